@@ -447,6 +447,164 @@ spax_status spax_greedy_allocation(const double* h_params, int n, double alpha, 
  */
 uint64_t spax_weight_bytes(int d_out, int full_fmt, int64_t n_full, int64_t n_approx);
 
+/*
+ * ---- The decode layer between its projections -------------------------------------------------
+ *
+ * Between two tiered projections of a decoder layer a token passes: the residual sum and the next
+ * norm (spax_residual_norm), the rotation by position and the write of its key and value into the
+ * cache (spax_kv_append), and the attention over that cache (spax_paged_attention). The pages name
+ * these only as what surrounds the projections (eigenradar commentary: the key-value cache stays on
+ * the GPU). One layer: norm -> masked GEMV (qkv) -> append -> attention -> masked GEMV (o) -> norm
+ * -> masked GEMV (gate/up) -> masked GEMV (down, _swiglu). Activations are fp32 throughout, as the
+ * GEMVs take and give them; the calls also take batches and prompts (one row for each token).
+ * Values are not checked for being finite: a NaN or Inf goes through the formulas.
+ */
+
+typedef enum { SPAX_KV_BF16 = 0, SPAX_KV_E4M3 = 1 } spax_kv_dtype;
+typedef enum { SPAX_NORM_RMS = 0, SPAX_NORM_LAYER = 1 } spax_norm_kind;
+typedef enum { SPAX_W_FP32 = 0, SPAX_W_BF16 = 1 } spax_w_dtype;
+
+/*
+ * A paged key-value cache of one layer, owned by the caller (device memory). Element (page, row,
+ * head, i) of the keys is at d_k + page * page_stride + row * token_stride + head * head_stride + i,
+ * strides in elements (64-bit offsets); the values likewise at d_v. Any order of the three outer
+ * dimensions works, and keys and values may share one allocation (not an element). A sequence's
+ * token at position p is in row p % page_size of page table[p / page_size].
+ *   BF16: elements are bf16, the scales must be 1.
+ *   E4M3: elements are 8-bit floats (4 exponent bits, 3 mantissa bits, largest value 448, no
+ *         infinity); an element stands for its value times k_scale (v_scale), both finite and > 0.
+ * Requires n_pages, page_size, n_kv_heads >= 1, head_dim a multiple of 16 up to 256; d_k, d_v and
+ * every stride of a dimension longer than 1 a multiple of 16 bytes, and those strides at least
+ * head_dim.
+ */
+typedef struct {
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t dtype; /* spax_kv_dtype */
+  float k_scale;
+  float v_scale;
+  int32_t reserved;
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  void* d_k;
+  void* d_v;
+} spax_kv_cache;
+
+/*
+ * Rotation by position: of the first rot_dim entries of a head, pair i (of rot_dim / 2) is turned by
+ * the angle pos * f_i, (a, b) -> (a cos - b sin, b cos + a sin); the rest stays. Pair i is entries
+ * (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved. d_inv_freq: fp64 [rot_dim / 2] (device),
+ * the f_i in radians per position with any scaling already applied. The angle is reduced in fp64,
+ * so far positions keep their accuracy. rot_dim a multiple of 8, 0 <= rot_dim <= head_dim; 0 turns
+ * nothing (d_inv_freq may be NULL).
+ */
+typedef struct {
+  int32_t rot_dim;
+  int32_t interleaved;
+  const double* d_inv_freq;
+} spax_rope;
+
+/*
+ * spax_kv_append — rotate q and k by their tokens' positions and write k and v into the cache.
+ * Token t of n_tok has n_heads query heads at d_q + t * q_stride, n_kv_heads key heads at d_k + t *
+ * k_stride and value heads at d_v + t * v_stride (fp32, heads contiguous; strides in floats), so the
+ * three may be parts of one qkv row. It is at position d_pos[t] of sequence d_seq[t]; with d_seq NULL
+ * it is of sequence t (then n_tok <= n_seq). d_page_table: int32 [n_seq][max_pages].
+ *   q: written rotated, fp32, to d_q_out + t * q_out_stride (d_q_out may equal d_q with the same
+ *      stride: in place). d_q NULL: no query heads (n_heads 0, d_q_out not used).
+ *   k: rotated in fp32, then rounded once to the cache's type; v: rounded. E4M3 stores
+ *      round(value / scale), |value / scale| above 448 (infinities too) as 448 with its sign.
+ * d_pos[t] < 0 marks padding: nothing of the token is written (cache and q row stay as they were).
+ * A sequence outside [0, n_seq), a position at or past max_pages * page_size or a page outside
+ * [0, n_pages) does the same and sets *d_status = SPAX_ERR_INDEX. The tokens' (page, row) places in
+ * one call must differ; where two agree, that row's contents are unspecified.
+ * Requires h_rope (NULL: no rotation) as above; d_q, d_k, d_v, d_q_out 16-byte aligned, strides
+ * multiples of 4 and at least the row when n_tok > 1; n_tok >= 0 (0: nothing is done); max_pages *
+ * page_size < 2^31. No workspace.
+ */
+spax_status spax_kv_append(const spax_kv_cache* h_cache, const float* d_q, int64_t q_stride,
+                           const float* d_k, int64_t k_stride, const float* d_v, int64_t v_stride,
+                           int n_tok, int n_heads, const int32_t* d_seq, const int32_t* d_pos,
+                           const int32_t* d_page_table, int n_seq, int max_pages,
+                           const spax_rope* h_rope, float* d_q_out, int64_t q_out_stride,
+                           int32_t* d_status, void* stream);
+
+/*
+ * Scores of spax_paged_attention: s_j = scale * (q . k_j), then softcap * tanh(s_j / softcap) when
+ * softcap > 0. window > 0: only the last `window` positions are seen; 0: all. scale finite,
+ * softcap >= 0 and finite, window >= 0.
+ */
+typedef struct {
+  float scale;
+  float softcap;
+  int32_t window;
+} spax_attn_params;
+
+/*
+ * spax_paged_attention — attention of one new token of each sequence over the paged cache.
+ * Sequence i's token has n_heads query heads (fp32, rotated) at d_q + i * q_stride; query head h
+ * reads key-value head h / (n_heads / n_kv_heads). It sees cached positions j in
+ * [max(0, L - window), L), L = d_seq_lens[i] (its own key and value appended before the call):
+ *   d_out[i][h] = sum_j softmax(s)_j v_j (fp32 [n_seq][n_heads][head_dim], fully written),
+ *   d_lse[i][h] = ln sum_j exp(s_j) (fp32 [n_seq][n_heads], may be NULL).
+ * L = 0 gives out = 0 and lse = -inf, and so does a row whose scores are all -inf. Rows of the
+ * cache past L, and outside the window, are not read: what they hold cannot matter.
+ * L outside [0, max_pages * page_size] is taken as 0, a page outside [0, n_pages) as not seen, and
+ * either sets *d_status = SPAX_ERR_INDEX.
+ * Products and sums are in fp32 (queries and probabilities enter the matrix instructions in parts
+ * that together hold their fp32 value); the split over the length depends on the lengths and the
+ * GPU model alone, and its parts are joined in a fixed order: the same bits on every run.
+ * Workspace: spax_attention_workspace_bytes() bytes, ZEROED BEFORE FIRST USE; every completed call
+ * leaves its counters at zero (zero it again after a device error). Calls that share a workspace
+ * must not run concurrently. No CTA waits for another.
+ * Requires n_heads a multiple of n_kv_heads, q_stride a multiple of 4 and at least n_heads *
+ * head_dim when n_seq > 1, d_q and d_out 16-byte aligned and not overlapping, n_seq >= 0 (0: nothing
+ * is done), max_pages * page_size < 2^31.
+ */
+spax_status spax_paged_attention(const spax_kv_cache* h_cache, const float* d_q, int64_t q_stride,
+                                 int n_seq, int n_heads, const int32_t* d_page_table,
+                                 int max_pages, const int32_t* d_seq_lens,
+                                 const spax_attn_params* h_params, float* d_out, float* d_lse,
+                                 int32_t* d_status, void* d_ws, size_t ws_bytes, void* stream);
+
+/*
+ * Device workspace bytes of spax_paged_attention on the CURRENT device, for any lengths and any
+ * number of sequences; 0 for an unsupported head layout.
+ */
+size_t spax_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim);
+
+/*
+ * A norm over the d entries of a row z. RMS: z / sqrt(mean(z^2) + eps). LAYER: (z - mean(z)) /
+ * sqrt(mean((z - mean(z))^2) + eps). Then times d_weight and plus d_bias ([d] of w_dtype on the
+ * device; NULL: none). eps >= 0.
+ */
+typedef struct {
+  int32_t kind;    /* spax_norm_kind */
+  int32_t w_dtype; /* spax_w_dtype of d_weight and d_bias */
+  const void* d_weight;
+  const void* d_bias;
+  float eps;
+} spax_norm;
+
+/*
+ * spax_residual_norm — the step between two blocks, for each of n_tok rows of d entries (fp32):
+ *   r = res_scale * h + out_scale * gate * N_post(y),   x = N_pre(r).
+ * h: the residual stream; y: the block's output (NULL: the sum is res_scale * h alone, for a
+ * model's first norm); h_post NULL: y as it is; d_gate NULL: 1, else fp32 [d] shared by all rows
+ * (gate_stride 0) or one row for each token (gate_stride >= d). d_r (NULL: not written) may be d_h or d_y;
+ * d_x (NULL: not written, h_pre not used) may be d_y or d_h; h_pre NULL with d_x set: x = r. d_r
+ * and d_x must differ, and at least one is given. Rows are contiguous. Statistics are in fp32 over
+ * values held on the chip, the mean before the deviations.
+ * Requires 1 <= d <= 32768, n_tok >= 0 (0: nothing is done), finite scales.
+ */
+spax_status spax_residual_norm(const float* d_h, const float* d_y, int n_tok, int d,
+                               const spax_norm* h_post, const float* d_gate, int64_t gate_stride,
+                               float res_scale, float out_scale, const spax_norm* h_pre,
+                               float* d_r, float* d_x, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -45,14 +45,6 @@ cudaError_t ensure_smem_limit(const void* kernel, int bytes) {
 
 // Dynamic shared memory a masked GEMV may use (227 KB per CTA, less room for static variables).
 
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-static spax_status launch_status(cudaError_t e) {
-  if (e == cudaSuccess) return SPAX_OK;
-  (void)cudaGetLastError();  // the error is reported through the status; clear the sticky-free one
-  return SPAX_ERR_CUDA;
-}
-
 }  // namespace spax
 
 using namespace spax;

@@ -68,6 +68,52 @@ cudaError_t launch_output_change(const float* y, const float* y_ref, int n, doub
 cudaError_t launch_calibrate(const float* X, long long M, long long idx_skip, long long idx_full,
                              float* t_out, int32_t* status, void* ws, cudaStream_t stream);
 
+// The decode layer between its projections (arguments checked by the entry points).
+struct AppendLaunch {
+  spax_kv_cache cache;
+  spax_rope rope;
+  const float *q, *k, *v;
+  float* q_out;
+  long long q_stride, k_stride, v_stride, q_out_stride;
+  const int32_t *seq, *pos, *table;
+  int32_t* status;
+  int n_tok, n_heads, n_seq, max_pages;
+};
+cudaError_t launch_kv_append(const AppendLaunch& a, cudaStream_t stream);
+
+struct AttnLaunch {
+  spax_kv_cache cache;
+  spax_attn_params prm;
+  const float* q;
+  long long q_stride;
+  const int32_t *table, *lens;
+  float *out, *lse;
+  int32_t* status;
+  void* ws;
+  int n_seq, n_heads, max_pages;
+};
+size_t attention_ws_bytes(int n_heads, int n_kv_heads, int head_dim, int sm_count);
+cudaError_t launch_paged_attention(const AttnLaunch& a, int sm_count, cudaStream_t stream);
+
+struct NormLaunch {
+  spax_norm post, pre;
+  bool has_post, has_pre;
+  const float *h, *y, *gate;
+  float *r, *x;
+  long long gate_stride;
+  float res_scale, out_scale;
+  int n_tok, d;
+};
+cudaError_t launch_residual_norm(const NormLaunch& a, cudaStream_t stream);
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline spax_status launch_status(cudaError_t e) {
+  if (e == cudaSuccess) return SPAX_OK;
+  (void)cudaGetLastError();  // the error is reported through the status; clear the sticky-free one
+  return SPAX_ERR_CUDA;
+}
+
 // Launch helper: every libspax kernel is launched as a programmatic dependent of its
 // predecessor in the stream (it calls griddepcontrol.wait before touching global memory).
 template <typename... KArgs, typename... Args>

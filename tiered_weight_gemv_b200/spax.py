@@ -27,6 +27,8 @@ FULL_BF16, FULL_INT4_G128 = 0, 1
 MASK_THRESHOLD, MASK_TOPK, MASK_GUIDED, MASK_TOPK_SCALED = 0, 1, 2, 3
 OP_TIERED_GEMV, OP_DENSE_GEMV, OP_CALIBRATE = 0, 1, 2
 MASK_MAX_DIN = 32768
+KV_BF16, KV_E4M3 = 0, 1
+NORM_RMS, NORM_LAYER = 0, 1
 
 
 class SpaxError(RuntimeError):
@@ -48,7 +50,34 @@ class spax_packed(ctypes.Structure):
                 ("d_approx", ctypes.c_void_p)]
 
 
+class spax_kv_cache(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("d_k", ctypes.c_void_p),
+                ("d_v", ctypes.c_void_p)]
+
+
+class spax_rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("d_inv_freq", ctypes.c_void_p)]
+
+
+class spax_attn_params(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("window", ctypes.c_int32)]
+
+
+class spax_norm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("d_weight", ctypes.c_void_p), ("d_bias", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_L = ctypes.c_int64
 _SIGS = {
     "spax_abi_version": ([], _I),
     "spax_status_string": ([_I], ctypes.c_char_p),
@@ -83,6 +112,11 @@ _SIGS = {
     "spax_weight_bytes": ([_I, _I, ctypes.c_int64, ctypes.c_int64], ctypes.c_uint64),
     "spax_greedy_allocation": ([_P, _I, ctypes.c_double, ctypes.c_double, ctypes.c_double, _P, _P,
                                 _I, _P, _P, _P], _I),
+    "spax_kv_append": ([_P, _P, _L, _P, _L, _P, _L, _I, _I, _P, _P, _P, _I, _I, _P, _P, _L, _P,
+                        _P], _I),
+    "spax_paged_attention": ([_P, _P, _L, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _Z, _P], _I),
+    "spax_attention_workspace_bytes": ([_I, _I, _I], _Z),
+    "spax_residual_norm": ([_P, _P, _I, _I, _P, _P, _L, _F, _F, _P, _P, _P, _P], _I),
 }
 for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -435,3 +469,233 @@ def alloc_workspace(op: int, d_out: int, d_in: int, device="cuda") -> torch.Tens
     if n == 0:
         raise SpaxError("spax_workspace_bytes", ERR_SHAPE)
     return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+# ------------------------------------------------------------- the decode layer between projections
+
+def _on(dev: int, t, dtype, name: str) -> int:
+    """The address of a tensor of the call's device (None: a null pointer); rows may be strided."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    return t.data_ptr()
+
+
+def _whole(dev: int, t, dtype, name: str) -> int:
+    if t is not None and isinstance(t, torch.Tensor) and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _on(dev, t, dtype, name)
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+
+
+def _heads(t: torch.Tensor, name: str):
+    """[tokens, heads, head_dim] whose heads are contiguous; the tokens' stride is free."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    n, h, d = t.shape
+    if t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}'s heads must be contiguous within a token")
+    return n, h, t.stride(0)
+
+
+class KvCache:
+    """A paged key-value cache of one layer: keys and values as [n_pages, page_size, n_kv_heads,
+    head_dim] tensors of bfloat16 or float8_e4m3fn, views with any order of the outer dimensions
+    (both with the same strides). An 8-bit element stands for its value times k_scale / v_scale."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: float = 1.0,
+                 v_scale: float = 1.0):
+        kinds = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3}
+        if not k.is_cuda or not v.is_cuda or k.device != v.device:
+            raise TypeError("the cache's pools must be CUDA tensors of one device")
+        if k.dtype not in kinds or k.dtype != v.dtype:
+            raise TypeError("the cache's pools must both be bfloat16 or both float8_e4m3fn")
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("the cache's pools must be [n_pages, page_size, n_kv_heads, head_dim] "
+                             "with the same strides, the last of them 1")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = k.shape
+        self.dtype, self.device = kinds[k.dtype], k.device
+        self._desc = spax_kv_cache(*k.shape, self.dtype, k_scale, v_scale, 0, *k.stride()[:3],
+                                   k.data_ptr(), v.data_ptr())
+        self._ref = ctypes.byref(self._desc)
+
+    def desc(self) -> spax_kv_cache:
+        return self._desc
+
+
+def alloc_kv_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
+                   dtype: int = KV_BF16, heads_first: bool = False, k_scale: float = 1.0,
+                   v_scale: float = 1.0, device="cuda") -> KvCache:
+    """A zeroed cache; heads_first lays a page out as [n_kv_heads][page_size][head_dim]."""
+    t = {KV_BF16: torch.bfloat16, KV_E4M3: torch.float8_e4m3fn}[dtype]
+    shape = ((n_pages, n_kv_heads, page_size, head_dim) if heads_first
+             else (n_pages, page_size, n_kv_heads, head_dim))
+    k, v = (torch.zeros(shape, dtype=torch.uint8 if dtype == KV_E4M3 else t,
+                        device=device).view(t) for _ in range(2))
+    if heads_first:
+        k, v = k.transpose(1, 2), v.transpose(1, 2)
+    return KvCache(k, v, k_scale, v_scale)
+
+
+class Rope:
+    """Rotation by position: inv_freq, fp64 [rot_dim / 2] on the device, the radians per position
+    of each pair; pairs (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved."""
+
+    def __init__(self, inv_freq: torch.Tensor, interleaved: bool = False):
+        dev = inv_freq.get_device() if inv_freq.is_cuda else -1
+        ptr = _whole(dev, inv_freq, torch.float64, "inv_freq")
+        self.inv_freq, self.interleaved = inv_freq, bool(interleaved)
+        self._desc = spax_rope(2 * inv_freq.numel(), int(self.interleaved), ptr)
+        self._ref = ctypes.byref(self._desc)
+
+
+class Norm:
+    """A norm's kind (NORM_RMS or NORM_LAYER), eps, and its weight and bias ([d], both fp32 or both
+    bf16; None: none)."""
+
+    def __init__(self, weight=None, bias=None, eps: float = 1e-5, kind: int = NORM_RMS):
+        given = [t for t in (weight, bias) if t is not None]
+        types = {t.dtype for t in given} or {torch.float32}
+        if len(types) != 1 or not types <= {torch.float32, torch.bfloat16}:
+            raise TypeError("weight and bias must both be float32 or both bfloat16")
+        if len({t.numel() for t in given}) > 1:
+            raise ValueError("weight and bias must have the same size")
+        self.weight, self.bias, self.eps, self.kind = weight, bias, eps, kind
+        self.d = given[0].numel() if given else None
+        self.device = given[0].get_device() if given else None
+        dt = types.pop()
+        ptrs = [_whole(self.device, t, dt, n) if t is not None else 0
+                for t, n in ((weight, "weight"), (bias, "bias"))]
+        self._desc = spax_norm(kind, int(dt == torch.bfloat16), *ptrs, eps)
+        self._ref = ctypes.byref(self._desc)
+
+    def _for(self, d: int, dev: int):
+        if self.d is not None and (self.d != d or self.device != dev):
+            raise ValueError(f"the norm's weight has {self.d} entries on cuda:{self.device}, "
+                             f"the rows {d} on cuda:{dev}")
+        return self._ref
+
+
+def _table(t: torch.Tensor, n_seq: int):
+    if t.dim() != 2 or t.shape[0] < n_seq:
+        raise ValueError("page_table must be [sequences, pages]")
+    return t.shape
+
+
+def spax_kv_append(cache: KvCache, q, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
+                   page_table: torch.Tensor, status: torch.Tensor, rope=None, seq=None, q_out=None,
+                   stream=None) -> None:
+    """Rotate q and k by pos and write k and v into the cache. q [tokens, heads, head_dim], k and v
+    [tokens, n_kv_heads, head_dim], fp32, the tokens' strides free (parts of one qkv row); q None:
+    keys and values alone. q_out None: q is rotated in place. pos, seq int32 [tokens] (seq None:
+    token t is of sequence t), page_table int32 [sequences, pages]; pos < 0 marks padding."""
+    dev = torch.cuda.current_device()
+    f32, i32 = torch.float32, torch.int32
+    n, kh, ks = _heads(k, "k")
+    nv, vh, vs = _heads(v, "v")
+    H = qs = os_ = 0
+    if q is not None:
+        nq, H, qs = _heads(q, "q")
+        if q_out is None:
+            q_out = q
+        if q_out.shape != q.shape or nq != n or q.shape[2] != cache.head_dim:
+            raise ValueError("q / q_out sizes do not match k or the cache")
+        os_ = _heads(q_out, "q_out")[2]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if (nv != n or kh != cache.n_kv_heads or vh != kh or k.shape[2] != cache.head_dim
+            or v.shape[2] != cache.head_dim or pos.numel() != n
+            or (seq is not None and seq.numel() != n)):
+        raise ValueError("k / v / pos / seq sizes do not match the cache or one another")
+    n_seq, max_pages = _table(page_table, n if seq is None else 0)
+    st = _lib.spax_kv_append(
+        cache._ref if cache.device.index == dev else _on(dev, cache.k, cache.k.dtype, "cache"),
+        _on(dev, q, f32, "q"), qs, _on(dev, k, f32, "k"), ks, _on(dev, v, f32, "v"), vs, n, H,
+        _whole(dev, seq, i32, "seq"), _whole(dev, pos, i32, "pos"),
+        _whole(dev, page_table, i32, "page_table"), n_seq, max_pages,
+        None if rope is None else _rope_on(rope, dev), _on(dev, q_out, f32, "q_out"), os_,
+        _whole(dev, status, i32, "status"), _raw_stream(stream, dev))
+    if st:
+        raise SpaxError("spax_kv_append", st)
+
+
+def _rope_on(rope: Rope, dev: int):
+    if rope.inv_freq.get_device() != dev:
+        _on(dev, rope.inv_freq, torch.float64, "inv_freq")
+    return rope._ref
+
+
+def spax_attention_workspace_bytes(n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(_lib.spax_attention_workspace_bytes(n_heads, n_kv_heads, head_dim))
+
+
+def alloc_attention_workspace(cache: KvCache, n_heads: int) -> torch.Tensor:
+    """A zeroed workspace of spax_paged_attention for this cache's layout, any lengths."""
+    with torch.cuda.device(cache.device):
+        n = spax_attention_workspace_bytes(n_heads, cache.n_kv_heads, cache.head_dim)
+    if n == 0:
+        raise SpaxError("spax_attention_workspace_bytes", ERR_SHAPE)
+    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
+
+
+def spax_paged_attention(cache: KvCache, q: torch.Tensor, page_table: torch.Tensor,
+                         seq_lens: torch.Tensor, out: torch.Tensor, status: torch.Tensor,
+                         ws: torch.Tensor, scale: float, window: int = 0, softcap: float = 0.0,
+                         lse=None, stream=None) -> None:
+    """Attention of one new token of each sequence over the cache: q fp32 [sequences, heads,
+    head_dim] (the sequences' stride free), seq_lens int32 [sequences] counting the new token, out
+    fp32 as q, contiguous; lse (optional) fp32 [sequences, heads]."""
+    dev = torch.cuda.current_device()
+    f32, i32 = torch.float32, torch.int32
+    n, H, qs = _heads(q, "q")
+    if q.shape[2] != cache.head_dim or out.shape != q.shape or seq_lens.numel() != n:
+        raise ValueError("q / out / seq_lens sizes do not match the cache or one another")
+    if lse is not None and lse.numel() != n * H:
+        raise ValueError("lse must be [sequences, heads]")
+    max_pages = _table(page_table, n)[1]
+    prm = spax_attn_params(scale, softcap, window)
+    st = _lib.spax_paged_attention(
+        cache._ref if cache.device.index == dev else _on(dev, cache.k, cache.k.dtype, "cache"),
+        _on(dev, q, f32, "q"), qs, n, H, _whole(dev, page_table, i32, "page_table"), max_pages,
+        _whole(dev, seq_lens, i32, "seq_lens"), ctypes.byref(prm), _whole(dev, out, f32, "out"),
+        _whole(dev, lse, f32, "lse"), _whole(dev, status, i32, "status"),
+        _whole(dev, ws, torch.uint8, "ws"), ws.numel(), _raw_stream(stream, dev))
+    if st:
+        raise SpaxError("spax_paged_attention", st)
+
+
+def spax_residual_norm(h: torch.Tensor, y, r, x, pre=None, post=None, gate=None,
+                       res_scale: float = 1.0, out_scale: float = 1.0, stream=None) -> None:
+    """r = res_scale h + out_scale gate N_post(y), x = N_pre(r) by rows: h, y, r, x fp32
+    [..., d] of the same size (y None: r = res_scale h; r or x None: not written; r and x may be h
+    or y), gate fp32 [d] for all rows or one row each, pre and post a Norm or None."""
+    dev = torch.cuda.current_device()
+    f32 = torch.float32
+    d = h.shape[-1] if h.dim() else 0
+    if d == 0:
+        raise ValueError("rows must have entries")
+    n = h.numel() // d
+    for t, name in ((y, "y"), (r, "r"), (x, "x")):
+        if t is not None and t.shape != h.shape:
+            raise ValueError(f"{name}'s size does not match h")
+    gs = 0
+    if gate is not None:
+        if gate.shape[-1] != d or gate.numel() not in (d, n * d):
+            raise ValueError("gate must be [d] or of h's size")
+        gs = d if gate.numel() == n * d and gate.dim() > 1 else 0
+    st = _lib.spax_residual_norm(
+        _whole(dev, h, f32, "h"), _whole(dev, y, f32, "y"), n, d,
+        None if post is None else post._for(d, dev), _whole(dev, gate, f32, "gate"), gs, res_scale,
+        out_scale, None if pre is None else pre._for(d, dev), _whole(dev, r, f32, "r"),
+        _whole(dev, x, f32, "x"), _raw_stream(stream, dev))
+    if st:
+        raise SpaxError("spax_residual_norm", st)
