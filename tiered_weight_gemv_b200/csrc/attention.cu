@@ -35,6 +35,7 @@ namespace spax {
 
 constexpr int kTile = 16;  // positions in a warp's tile, starting at a multiple of 16
 constexpr int kUnit = 64;  // positions in a unit of work, starting at a multiple of 64
+constexpr int kJoin = 16;  // parts that are joined in one step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Shapes of one instance: head_dim padded to DP, NT blocks of 8 query heads, WARPS warps with rings
@@ -138,7 +139,7 @@ struct AttnArgs {
   bool page16;        // a tile's positions are on one page
   float* part;        // [2 CTAs][HB][DP] outputs of shared rows
   float2* part_ml;    // [2 CTAs][HB] their maxima and sums
-  uint32_t* tickets;  // [2 CTAs], zero at rest
+  uint32_t *tickets, *tickets2;  // [2 CTAs] each, zero at rest
 };
 
 template <class S>
@@ -160,6 +161,85 @@ struct Attn {
     return g.page_shift < 0 ? pos : (int)(__umulhi((uint32_t)pos, g.page_mul) >> g.page_shift);
   }
 };
+
+// Counts this CTA in: true for the last of n, which also readies the ticket for the next call. The
+// parts that the others wrote before are visible to every thread of it.
+__device__ __forceinline__ bool arrive(uint32_t* ticket, int n, bool* is_last) {
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    *is_last = atomicAdd(ticket, 1u) == (uint32_t)(n - 1);
+    if (*is_last) *ticket = 0;
+    __threadfence();
+  }
+  __syncthreads();
+  return *is_last;
+}
+
+// One head's entries of a row, joined: written as they are to a slot, or divided to the output.
+template <class S>
+__device__ __forceinline__ void put_row(const AttnArgs& g, int slot, long long at, int h, int d, float4 v,
+                                        float M, float L) {
+  if (slot >= 0) {
+    __stcg(reinterpret_cast<float4*>(g.part + ((long long)slot * S::HB + h) * S::DP + d), v);
+    if (d == 0) __stcg(g.part_ml + slot * S::HB + h, make_float2(M, L));
+  } else {
+    const float inv = L == 0.0f ? 0.0f : g.a.cache.v_scale / L;
+    if (L == 0.0f) v = make_float4(0, 0, 0, 0);
+    v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+    *reinterpret_cast<float4*>(g.a.out + (at + h) * g.a.cache.head_dim + d) = v;
+    if (d == 0 && g.a.lse) g.a.lse[at + h] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+  }
+}
+
+// Joins n parts of a row, the slots of which slot_of gives, in their order.
+template <class S, class F>
+__device__ __forceinline__ void join(const AttnArgs& g, uint8_t* smem, int heads, int n, F slot_of,
+                                     int to, long long at) {
+  float2* ml = reinterpret_cast<float2*>(smem);  // [n][HB]: maximum and sum, then weight and sum
+  __shared__ float2 total[S::HB];
+  const int tid = threadIdx.x;
+  for (int e = tid; e < n * S::HB; e += S::THREADS)
+    if (e % S::HB < heads) ml[e] = __ldcg(g.part_ml + slot_of(e / S::HB) * S::HB + e % S::HB);
+  __syncthreads();
+  if (tid < heads) {
+    float M = -INFINITY, L = 0.0f;
+    for (int k = 0; k < n; ++k) M = fmaxf(M, ml[k * S::HB + tid].x);  // drops NaN: its sum has it too
+    for (int k = 0; k < n; ++k) {
+      const float2 v = ml[k * S::HB + tid];
+      const float f = v.x == -INFINITY ? 0.0f : exp2_ftz(v.x - M);
+      L += f * v.y;
+      ml[k * S::HB + tid].x = f;
+    }
+    total[tid] = make_float2(M, L);
+  }
+  __syncthreads();
+  const int quads = g.a.cache.head_dim / 4;
+  for (int e = tid; e < heads * quads; e += S::THREADS) {
+    const int h = e / quads, d = (e - h * quads) * 4;
+    const float4* src = reinterpret_cast<const float4*>(g.part + (long long)h * S::DP + d);
+    float4 v = make_float4(0, 0, 0, 0);
+    int k = 0;
+    auto take = [&](auto count) {
+      constexpr int N = decltype(count)::value;
+      for (; k + N <= n; k += N) {
+        float4 t[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) t[i] = __ldcg(src + (long long)slot_of(k + i) * (S::HB * S::DP / 4));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float f = ml[(k + i) * S::HB + h].x;
+          v.x += f * t[i].x, v.y += f * t[i].y, v.z += f * t[i].z, v.w += f * t[i].w;
+        }
+      }
+    };
+    take(std::integral_constant<int, 8>{});
+    take(std::integral_constant<int, 4>{});
+    take(std::integral_constant<int, 1>{});
+    put_row<S>(g, to, at, h, d, v, total[h].x, total[h].y);
+  }
+  __syncthreads();  // the buffers may be used again
+}
 
 template <class S>
 __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const AttnArgs g) {
@@ -631,17 +711,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
         L += f * warp_ml[w][h].y;
         v.x += f * t.x, v.y += f * t.y, v.z += f * t.z, v.w += f * t.w;
       }
-      const long long at = (long long)seq * g.a.n_heads + head0 + h;
-      if (whole) {
-        const float inv = L == 0.0f ? 0.0f : C.v_scale / L;
-        if (L == 0.0f) v = make_float4(0, 0, 0, 0);
-        v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-        *reinterpret_cast<float4*>(g.a.out + at * D + d) = v;
-        if (d == 0 && g.a.lse) g.a.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
-      } else {
-        *reinterpret_cast<float4*>(g.part + ((long long)slot * HB + h) * DP + d) = v;
-        if (d == 0) g.part_ml[slot * HB + h] = make_float2(M, L);
-      }
+      put_row<S>(g, whole ? -1 : slot, (long long)seq * g.a.n_heads + head0, h, d, v, M, L);
     }
 
     // ---- a shared row: the last CTA to arrive joins its parts ----------------------------------------
@@ -650,36 +720,21 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       const int n = b1 - b0 + 1;
       // the first CTA's slot: its first segment if its run starts in this row
       const int slot0 = 2 * b0 + (row_begin <= U * b0 / B ? 0 : 1);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        is_last = atomicAdd(g.tickets + slot0, 1u) == (uint32_t)(n - 1);
-        if (is_last) g.tickets[slot0] = 0;
-        __threadfence();
-      }
-      __syncthreads();
-      if (is_last) {
-        auto slot_of = [&](int k) { return k == 0 ? slot0 : 2 * (b0 + k); };
-        for (int e = tid; e < heads * quads; e += T) {
-          const int h = e / quads, d = (e - h * quads) * 4;
-          float M = -INFINITY, L = 0.0f;
-          for (int k = 0; k < n; ++k) M = fmaxf(M, __ldcg(g.part_ml + slot_of(k) * HB + h).x);
-          float4 v = make_float4(0, 0, 0, 0);
-          for (int k = 0; k < n; ++k) {
-            const float2 ml = __ldcg(g.part_ml + slot_of(k) * HB + h);
-            const float f = ml.x == -INFINITY ? 0.0f : exp2_ftz(ml.x - M);
-            if (f == 0.0f && ml.y == 0.0f) continue;
-            const float4 t = __ldcg(reinterpret_cast<const float4*>(
-                g.part + ((long long)slot_of(k) * HB + h) * DP + d));
-            L += f * ml.y;
-            v.x += f * t.x, v.y += f * t.y, v.z += f * t.z, v.w += f * t.w;
-          }
-          const float inv = L == 0.0f ? 0.0f : C.v_scale / L;
-          if (L == 0.0f) v = make_float4(0, 0, 0, 0);
-          v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-          const long long at = (long long)seq * g.a.n_heads + head0 + h;
-          *reinterpret_cast<float4*>(g.a.out + at * D + d) = v;
-          if (d == 0 && g.a.lse) g.a.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+      const long long at = (long long)seq * g.a.n_heads + head0;
+      auto slot_of = [&](int k) { return k == 0 ? slot0 : 2 * (b0 + k); };
+      // In one step up to kJoin parts; else groups of about sqrt(n) first, each by its own last CTA,
+      // into the slot of the group's first: two short reads in place of one long one.
+      int group = n;
+      if (n > kJoin)
+        for (group = kJoin / 2; group * group < n;) ++group;
+      const int k0 = (b - b0) / group * group, groups = (n + group - 1) / group;
+      bool last = arrive(g.tickets + slot_of(k0), min(group, n - k0), &is_last);
+      if (last) {
+        join<S>(g, smem, heads, min(group, n - k0), [&](int i) { return slot_of(k0 + i); },
+                groups == 1 ? -1 : slot_of(k0), at);
+        if (groups > 1) {
+          last = arrive(g.tickets2 + slot0, groups, &is_last);
+          if (last) join<S>(g, smem, heads, groups, [&](int i) { return slot_of(i * group); }, -1, at);
         }
       }
     }
@@ -703,7 +758,7 @@ static int padded_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 1
 size_t attention_ws_bytes(int n_heads, int n_kv_heads, int head_dim, int sm_count) {
   const size_t hb = 8 * head_blocks(n_heads / n_kv_heads, head_dim);
   const size_t slots = 2 * kMaxCtas * (size_t)sm_count;  // two for each CTA
-  return slots * hb * (padded_dim(head_dim) * 4 + 8) + ((slots * 4 + 255) & ~size_t(255));
+  return slots * hb * (padded_dim(head_dim) * 4 + 8) + ((slots * 8 + 255) & ~size_t(255));
 }
 
 template <class S>
@@ -714,7 +769,8 @@ static cudaError_t launch_shape(AttnArgs g, int sm_count, cudaStream_t stream) {
   g.blocks = (g.row_heads + S::HB - 1) / S::HB;
   const long long slots = 2ll * kMaxCtas * sm_count;
   g.tickets = static_cast<uint32_t*>(g.a.ws);
-  g.part = reinterpret_cast<float*>(static_cast<uint8_t*>(g.a.ws) + ((slots * 4 + 255) & ~255ll));
+  g.tickets2 = g.tickets + slots;
+  g.part = reinterpret_cast<float*>(static_cast<uint8_t*>(g.a.ws) + ((slots * 8 + 255) & ~255ll));
   g.part_ml = reinterpret_cast<float2*>(g.part + slots * S::HB * S::DP);
   long long longest = (long long)g.a.max_pages * g.a.cache.page_size;
   if (g.a.prm.window > 0 && g.a.prm.window + kUnit < longest) longest = g.a.prm.window + kUnit;
