@@ -6,13 +6,13 @@
 // enough bytes in flight.
 //
 // Work: a row is one (sequence, key head, block of up to 8 NT query heads). Its positions are cut
-// into units of 64; the units of all rows, laid end to end, are dealt to the CTAs of one wave in
-// equal contiguous runs, so ragged batches and single long sequences both fill the GPU. A CTA's run
-// covers parts of rows (segments); a row that several CTAs share is joined by the last of them to
+// into units of 64, and the units of all rows are dealt to the CTAs of one wave in nearly equal runs,
+// so ragged batches and single long sequences both fill the GPU. A CTA's run covers a part of a row,
+// or parts of several (segments); a row that several CTAs share is joined by the last of them to
 // arrive, in the order of the CTAs, so the result does not depend on who that is. No CTA waits for
 // another.
 //
-// Within a segment the CTA's warps take tiles of 16 positions in turn; each streams its own
+// Within a segment the CTA's warps take tiles of 16 or 32 positions in turn; each streams its own
 // through its own ring in shared memory with 16-byte asynchronous copies, and keeps its own running
 // maximum, sum and outputs; the warps meet once, at the segment's end.
 //
@@ -33,25 +33,26 @@
 
 namespace spax {
 
-constexpr int kTile = 16;  // positions in a warp's tile, starting at a multiple of 16
 constexpr int kUnit = 64;  // positions in a unit of work, starting at a multiple of 64
 constexpr int kJoin = 16;  // parts that are joined in one step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Shapes of one instance: head_dim padded to DP, NT blocks of 8 query heads, WARPS warps with rings
-// of STAGES tiles, CTAS resident on an SM.
-template <int DP_, bool E4M3_, int NT_, int WARPS_, int STAGES_, int CTAS_>
+// Shapes of one instance: head_dim padded to DP, NT blocks of 8 query heads, tiles of 16 MT positions,
+// WARPS warps with rings of SLOTS pieces (a tile's keys or its values; an odd number, so that the
+// piece that is started before keys are used is keys again), CTAS resident on an SM.
+template <int DP_, bool E4M3_, int NT_, int MT_, int WARPS_, int SLOTS_, int CTAS_>
 struct AttnShape {
-  static constexpr int DP = DP_, NT = NT_, HB = 8 * NT_, STAGES = STAGES_, CTAS = CTAS_;
+  static constexpr int DP = DP_, NT = NT_, HB = 8 * NT_, MT = MT_, TILE = 16 * MT_, SLOTS = SLOTS_, CTAS = CTAS_;
   static constexpr int WARPS = WARPS_, THREADS = WARPS * 32;
   static constexpr bool E4M3 = E4M3_;
   static constexpr int ES = E4M3 ? 1 : 2;
   static constexpr int QP = 3, PP = E4M3 ? 2 : 3;  // parts of a query entry, of a probability
   static constexpr int ROW = DP * ES;             // bytes of a row of a tile
   static constexpr int CH = ROW / 16;             // 16-byte chunks of a row
-  static constexpr int HALF = kTile * ROW;        // bytes of a tile's keys (or values)
-  static constexpr int STAGE = 2 * HALF;
-  static constexpr int RING = WARPS * STAGES * STAGE;
+  static constexpr int PIECE = TILE * ROW;       // bytes of a tile's keys (or values)
+  static constexpr int AHEAD = (SLOTS - 1) / 2;   // tiles between a copy's start and its use
+  static constexpr int RING = WARPS * SLOTS * PIECE;
+  static_assert(SLOTS % 2 == 1 && SLOTS >= 3);
   static constexpr int KS = DP / 16;              // k steps of a score
   static constexpr int SMEM = RING + KS / 2 * QP * NT * 512;  // and the query's parts
   static constexpr int OS = DP + 4;               // row stride of the warps' outputs at the join
@@ -84,6 +85,13 @@ __device__ __forceinline__ float exp2_ftz(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// (x, y) += (a, b), two lanes an instruction.
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{ .reg .b64 p, q; mov.b64 p, {%0, %1}; mov.b64 q, {%2, %3}; add.rn.f32x2 p, p, q; mov.b64 {%0, %1}, p; }"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -130,13 +138,28 @@ __device__ __forceinline__ void finite_pairs(const uint32_t (&a)[4], uint32_t (&
     asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(f[k]) : "r"(a[k]), "r"(0x7F7F7F7Fu));
 }
 
+// tanh without branches, within a few ulp: (1 - u) / (1 + u) with u = e^(-2|x|), and below 0.4, where
+// that difference cancels, the odd Taylor series to x^13 (the next term is below 2^-25 of x there).
+__device__ __forceinline__ float tanh_flat(float x) {
+  const float a = fabsf(x), u = exp2_ftz(-2.0f * kLog2e * a);
+  const float big = copysignf(__fdividef(1.0f - u, 1.0f + u), x);
+  const float y = x * x;
+  float p = 21844.0f / 6081075.0f;
+  p = fmaf(p, y, -1382.0f / 155925.0f);
+  p = fmaf(p, y, 62.0f / 2835.0f);
+  p = fmaf(p, y, -17.0f / 315.0f);
+  p = fmaf(p, y, 2.0f / 15.0f);
+  p = fmaf(p, y, -1.0f / 3.0f);
+  return a < 0.4f ? fmaf(x * y, p, x) : big;
+}
+
 struct AttnArgs {
   AttnLaunch a;
   uint32_t page_mul;  // position / page_size = page_size == 1 ? position : umulhi(position, mul) >> shift
   int page_shift;
   int row_heads;      // query heads to a key head
   int blocks;         // blocks of HB query heads to a key head
-  bool page16;        // a tile's positions are on one page
+  bool page16;        // 16 positions from a multiple of 16 are on one page
   float* part;        // [2 CTAs][HB][DP] outputs of shared rows
   float2* part_ml;    // [2 CTAs][HB] their maxima and sums
   uint32_t *tickets, *tickets2;  // [2 CTAs] each, zero at rest
@@ -165,9 +188,9 @@ struct Attn {
 // Counts this CTA in: true for the last of n, which also readies the ticket for the next call. The
 // parts that the others wrote before are visible to every thread of it.
 __device__ __forceinline__ bool arrive(uint32_t* ticket, int n, bool* is_last) {
-  __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
+    __threadfence();
     *is_last = atomicAdd(ticket, 1u) == (uint32_t)(n - 1);
     if (*is_last) *ticket = 0;
     __threadfence();
@@ -192,65 +215,58 @@ __device__ __forceinline__ void put_row(const AttnArgs& g, int slot, long long a
   }
 }
 
-// Joins n parts of a row, the slots of which slot_of gives, in their order.
+// Joins n parts of a row, the slots of which slot_of gives, in their order: a thread takes the
+// maxima, sums and entries of eight parts at a time, all in flight at once.
 template <class S, class F>
-__device__ __forceinline__ void join(const AttnArgs& g, uint8_t* smem, int heads, int n, F slot_of,
-                                     int to, long long at) {
-  float2* ml = reinterpret_cast<float2*>(smem);  // [n][HB]: maximum and sum, then weight and sum
-  __shared__ float2 total[S::HB];
-  const int tid = threadIdx.x;
-  for (int e = tid; e < n * S::HB; e += S::THREADS)
-    if (e % S::HB < heads) ml[e] = __ldcg(g.part_ml + slot_of(e / S::HB) * S::HB + e % S::HB);
-  __syncthreads();
-  if (tid < heads) {
-    float M = -INFINITY, L = 0.0f;
-    for (int k = 0; k < n; ++k) M = fmaxf(M, ml[k * S::HB + tid].x);  // drops NaN: its sum has it too
-    for (int k = 0; k < n; ++k) {
-      const float2 v = ml[k * S::HB + tid];
-      const float f = v.x == -INFINITY ? 0.0f : exp2_ftz(v.x - M);
-      L += f * v.y;
-      ml[k * S::HB + tid].x = f;
-    }
-    total[tid] = make_float2(M, L);
-  }
-  __syncthreads();
+__device__ __forceinline__ void join(const AttnArgs& g, int heads, int n, F slot_of, int to, long long at) {
+  constexpr int N = 8;
   const int quads = g.a.cache.head_dim / 4;
-  for (int e = tid; e < heads * quads; e += S::THREADS) {
+  for (int e = threadIdx.x; e < heads * quads; e += S::THREADS) {
     const int h = e / quads, d = (e - h * quads) * 4;
-    const float4* src = reinterpret_cast<const float4*>(g.part + (long long)h * S::DP + d);
     float4 v = make_float4(0, 0, 0, 0);
-    int k = 0;
-    auto take = [&](auto count) {
-      constexpr int N = decltype(count)::value;
-      for (; k + N <= n; k += N) {
-        float4 t[N];
+    float M = -INFINITY, L = 0.0f;
+    for (int k = 0; k < n; k += N) {
+      float4 t[N];
+      float2 ml[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) t[i] = __ldcg(src + (long long)slot_of(k + i) * (S::HB * S::DP / 4));
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float f = ml[(k + i) * S::HB + h].x;
-          v.x += f * t[i].x, v.y += f * t[i].y, v.z += f * t[i].z, v.w += f * t[i].w;
-        }
+      for (int i = 0; i < N; ++i) {
+        const long long slot = slot_of(min(k + i, n - 1));
+        ml[i] = __ldcg(g.part_ml + slot * S::HB + h);
+        t[i] = __ldcg(reinterpret_cast<const float4*>(g.part + (slot * S::HB + h) * S::DP + d));
       }
-    };
-    take(std::integral_constant<int, 8>{});
-    take(std::integral_constant<int, 4>{});
-    take(std::integral_constant<int, 1>{});
-    put_row<S>(g, to, at, h, d, v, total[h].x, total[h].y);
+      float top = M;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (k + i >= n) ml[i] = make_float2(-INFINITY, 0.0f);
+        top = fmaxf(top, ml[i].x);  // drops a NaN: its sum is NaN too
+      }
+      const float fade = M == -INFINITY ? (L == 0.0f ? 0.0f : L) : exp2_ftz(M - top);  // L may be NaN
+      L *= fade;
+      v.x *= fade, v.y *= fade, v.z *= fade, v.w *= fade;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (ml[i].x == -INFINITY && ml[i].y == 0.0f) continue;  // nothing seen
+        const float f = ml[i].x == -INFINITY ? 0.0f : exp2_ftz(ml[i].x - top);
+        L += f * ml[i].y;
+        v.x += f * t[i].x, v.y += f * t[i].y, v.z += f * t[i].z, v.w += f * t[i].w;
+      }
+      M = top;
+    }
+    put_row<S>(g, to, at, h, d, v, M, L);
   }
-  __syncthreads();  // the buffers may be used again
 }
 
 template <class S>
 __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const AttnArgs g) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long prefix[S::THREADS + 1];
+  __shared__ long long prefix[S::WARPS];
   __shared__ long long start_base;
   __shared__ int start_seq;
   __shared__ float2 warp_ml[S::WARPS][S::HB];
   __shared__ bool is_last;
   using A = Attn<S>;
-  constexpr int DP = S::DP, NT = S::NT, HB = S::HB, T = S::THREADS, W = S::WARPS;
+  constexpr int DP = S::DP, NT = S::NT, HB = S::HB, T = S::THREADS, W = S::WARPS,
+                MT = S::MT, TILE = S::TILE;
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int r = lane >> 2, c = lane & 3;
@@ -263,64 +279,112 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- this CTA's run of units -----------------------------------------------------------------
-  const int per = (n_seq + T - 1) / T;
-  {
-    long long sum = 0;
+  // ---- this CTA's share ------------------------------------------------------------------------
+  // Where a run length gives every row whole CTAs of its own within the wave (runs start at row
+  // starts, the last of a row may be shorter), that is taken: one segment, one start-up and one
+  // join for each CTA. Else all units are dealt in equal runs across row ends.
+  auto units_at = [&](int s) {
+    bool bad;
+    return s < n_seq ? A::units_of(g, A::clipped_len(g, s, &bad)) : 0;
+  };
+  const bool few = n_seq <= 32;  // a lane for each sequence, and no barriers
+  const int per = few ? 1 : (n_seq + T - 1) / T, s0 = few ? lane : tid * per;
+  auto total = [&](auto f) -> long long {  // sum of f(units) over the sequences
+    if (few) return __reduce_add_sync(~0u, (unsigned)f(units_at(lane)));
+    long long x = 0;
+    for (int k = 0; k < per; ++k) x += f(units_at(s0 + k));
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    __syncthreads();
+    if (lane == 0) prefix[warp] = x;
+    __syncthreads();
+    x = 0;
+    for (int w = 0; w < W; ++w) x += prefix[w];
+    return x;
+  };
+  const long long U = rows_of_seq * total([](int u) { return u; });
+  long long B = min((long long)gridDim.x, U);
+  int run = 0;  // units in a run of the first kind
+  if (U > 0) {
+    const long long rows = rows_of_seq * total([](int u) { return u > 0; });
+    if (2 * rows <= gridDim.x) {
+      run = (int)((U + B - 1) / B);
+      // a run may be this much longer than equal runs before their row ends cost less
+      const int most = run + max(6, run / 8);
+      const int more = few ? max(1, run / 16) : (most - run) / 2;
+      for (;; run += more) {
+        const long long n = rows_of_seq * total([run](int u) { return (u + run - 1) / run; });
+        if (n <= gridDim.x) {
+          B = n;
+          break;
+        }
+        if (run >= most) {
+          run = 0;
+          break;
+        }
+      }
+    }
+  }
+  if (b == 0) {
     bool any_bad = false;
-    for (int s = tid * per; s < min(n_seq, (tid + 1) * per); ++s) {
+    for (int k = tid; k < n_seq; k += T) {
       bool bad;
-      sum += rows_of_seq * A::units_of(g, A::clipped_len(g, s, &bad));
+      A::clipped_len(g, k, &bad);
       any_bad |= bad;
     }
-    if (any_bad && b == 0) record_status(g.a.status, SPAX_ERR_INDEX);
+    if (any_bad) record_status(g.a.status, SPAX_ERR_INDEX);
+  }
+  // rows that see nothing
+  for (int s = b; s < n_seq; s += gridDim.x) {
+    if (units_at(s) != 0) continue;
+    for (int i = tid; i < g.a.n_heads * D; i += T) g.a.out[(long long)s * g.a.n_heads * D + i] = 0.0f;
+    if (g.a.lse)
+      for (int i = tid; i < g.a.n_heads; i += T) g.a.lse[(long long)s * g.a.n_heads + i] = -INFINITY;
+  }
+  if (b >= B) return;
+
+  // the sequence of the share's first unit (run), and the units (runs) before it
+  const long long begin = run ? b : U * b / B, end = run ? b + 1 : U * (b + 1) / B;
+  auto weight = [&](int s) {
+    const int u = units_at(s);
+    return rows_of_seq * (run ? (u + run - 1) / run : u);
+  };
+  int seq;
+  long long base;
+  {
+    const long long own = weight(s0);
+    long long sum = own;
+    for (int k = 1; k < per; ++k) sum += weight(s0 + k);
     long long x = sum;  // inclusive scan
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(~0u, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) prefix[warp] = x;
-    __syncthreads();
-    long long before = 0;
-    for (int w = 0; w < warp; ++w) before += prefix[w];
-    __syncthreads();
-    prefix[tid + 1] = before + x;
-    if (tid == 0) prefix[0] = 0;
-    __syncthreads();
-  }
-  const long long U = prefix[T];
-  const long long B = min((long long)gridDim.x, U);
-
-  // rows that see nothing
-  for (int s = b; s < n_seq; s += gridDim.x) {
-    bool bad;
-    if (A::units_of(g, A::clipped_len(g, s, &bad)) != 0) continue;
-    for (int i = tid; i < g.a.n_heads * D; i += T)
-      g.a.out[(long long)s * g.a.n_heads * D + i] = 0.0f;
-    if (g.a.lse)
-      for (int i = tid; i < g.a.n_heads; i += T)
-        g.a.lse[(long long)s * g.a.n_heads + i] = -INFINITY;
-  }
-  if (b >= B) return;
-
-  const long long begin = U * b / B, end = U * (b + 1) / B;
-  if (prefix[tid] <= begin && begin < prefix[tid + 1]) {
-    long long base = prefix[tid];
-    int s = tid * per;
-    for (;; ++s) {
-      bool bad;
-      const long long n = rows_of_seq * A::units_of(g, A::clipped_len(g, s, &bad));
-      if (begin < base + n) break;
-      base += n;
+    if (few) {
+      seq = __popc(__ballot_sync(~0u, x <= begin));
+      base = __shfl_sync(~0u, x - own, seq);
+    } else {
+      __syncthreads();
+      if (lane == 31) prefix[warp] = x;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) x += prefix[w];
+      if (x - sum <= begin && begin < x) {
+        long long at = x - sum;
+        int s = s0;
+        for (;; ++s) {
+          const long long n = weight(s);
+          if (begin < at + n) break;
+          at += n;
+        }
+        start_seq = s;
+        start_base = at;
+      }
+      __syncthreads();
+      seq = start_seq;
+      base = start_base;
     }
-    start_seq = s;
-    start_base = base;
   }
-  __syncthreads();
-  int seq = start_seq;
-  long long base = start_base;
 
-  const uint32_t ring = smem_u32(smem) + warp * (S::STAGES * S::STAGE);
+  const uint32_t ring = smem_u32(smem) + warp * (S::SLOTS * S::PIECE);
   const uint32_t qsm = smem_u32(smem) + S::RING;
 
   for (long long x = begin; x < end;) {
@@ -332,9 +396,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       continue;
     }
     const long long y = x - base;
-    const int row = (int)(y / units), u0 = (int)(y - (long long)row * units);
-    const int u1 = (int)min((long long)units, u0 + (end - x));
-    const long long row_begin = base + (long long)row * units, row_end = row_begin + units;
+    const int runs = run ? (units + run - 1) / run : units;  // the coordinate's extent of a row
+    const int row = (int)(y / runs), r0 = (int)(y - (long long)row * runs);
+    const int u0 = run ? r0 * run : r0;
+    const int u1 = (int)min((long long)units, u0 + (run ? run : end - x));
+    const long long row_begin = base + (long long)row * runs;
     const int kvh = row / g.blocks, hb = row - kvh * g.blocks;
     const int heads = min(HB, g.row_heads - hb * HB);   // real query heads of this block
     const int head0 = kvh * g.row_heads + hb * HB;
@@ -348,7 +414,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
     // ---- the query's parts, and the factors from a product to an exponent of two -----------------
     // k steps 2 i and 2 i + 1 of part p, block nt lie together: lane l's two fragments in 16 bytes.
     float f1[NT][2], f2;
-    {
+    auto prepare_query = [&] {
       const float cap = g.a.prm.softcap;
       f2 = cap * kLog2e;
 #pragma unroll
@@ -398,8 +464,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
         f1[nt][0] = __shfl_sync(~0u, f, (2 * c) * 4);
         f1[nt][1] = __shfl_sync(~0u, f, (2 * c + 1) * 4);
       }
-    }
-    __syncthreads();
+      __syncthreads();
+    };
 
     // ---- this warp's tiles: tile i starts at t0 + (i * W + warp) * 16 ------------------------------
     // Exponents are taken from a base that trails the maximum by up to kSlack powers of two (it moves
@@ -407,81 +473,103 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
     // parts stay normal numbers (and their sums are lowered again, exactly, at the end).
     constexpr float kSlack = S::E4M3 ? 3.0f : 8.0f, kLift = S::E4M3 ? 12.0f : 0.0f,
                     kDrop = S::E4M3 ? 1.0f / 4096.0f : 1.0f;
-    const int tiles = (t1 - t0 + kTile - 1) / kTile;
+    const int tiles = (t1 - t0 + TILE - 1) / TILE;
     const int mine = tiles > warp ? (tiles - warp + W - 1) / W : 0;
-    const int first = t0 + warp * kTile;
+    const int first = t0 + warp * TILE;
     float m[NT][2], l[NT][2], o[NT][DP / 16][4];
 
     auto stream = [&](auto careful) {
       constexpr bool CAREFUL = decltype(careful)::value;
+      const int mine_at = lane & (TILE - 1);  // this lane's position in a tile
       auto page_entry = [&](int i) {  // the table's entry for the lane's position of tile i
-        int pos = first + i * (W * kTile);
-        if (!g.page16) pos = min(pos + (lane & 15), t1 - 1);
-        return i < mine ? __ldg(table + A::page_of(g, pos)) : 0;
+        int pos = first + i * (W * TILE) + (g.page16 ? mine_at & 16 : mine_at);
+        return i < mine ? __ldg(table + A::page_of(g, min(pos, t1 - 1))) : 0;
       };
-      // Starts the copies of tile i; returns which of its positions are seen.
-      auto issue = [&](int i, int page) -> uint32_t {
-        uint32_t bits = 0;
-        if (i < mine) {
-          const int pos0 = first + i * (W * kTile);
-          const uint32_t stage = ring + (uint32_t)i % S::STAGES * S::STAGE;
-          constexpr int RPI = 32 / S::CH >= 1 ? 32 / S::CH : 1;  // rows of a step
-          const int row0 = lane / S::CH, ch = lane % S::CH;
-          auto put = [&](int k, const uint8_t* ks, const uint8_t* vs, bool real) {
-            const int row_ = k * RPI + row0;
-            // keys: rows of unlike parity in different halves of the banks; values: pairs of rows
-            const int kc = S::CH >= 8 ? ch ^ ((row_ & 1) << 2) : ch;
-            const int vc = S::CH >= 8 ? ch ^ (((row_ >> 1) & 3) << 1) : ch ^ (((row_ >> 1) & 1) << 1);
-            cp16(stage + row_ * S::ROW + kc * 16, ks, real);
-            cp16(stage + S::HALF + row_ * S::ROW + vc * 16, vs, real);
-          };
-          if (g.page16 && pos0 >= lo && pos0 + kTile <= t1 && (uint32_t)page < (uint32_t)C.n_pages &&
-              D == DP) {
-            // the whole tile on one page: rows at one stride
-            const long long at = (page * C.page_stride +
-                                  (long long)(pos0 - A::page_of(g, pos0) * C.page_size + row0) * C.token_stride) * S::ES + ch * 16;
-            const uint8_t* ks = kpool + at;
-            const uint8_t* vs = vpool + at;
-            const long long step = RPI * C.token_stride * S::ES;
-            bits = 0xFFFFu;
+      // Where the rows of tile i are, and which of its positions are seen.
+      struct Place {
+        long long off[MT];  // one page for each 16: pool offset of this lane's chunk of its first row;
+                            // else off[0]: of this lane's position, or -1
+        uint32_t bits;
+        bool plain;
+      };
+      constexpr uint32_t kAll = TILE == 32 ? ~0u : (1u << TILE) - 1;
+      constexpr int RPI = 32 / S::CH;  // rows of a copy step
+      const int row0 = lane / S::CH, ch = lane % S::CH;
+      auto place = [&](int i, int page) {
+        Place at;
+        at.off[0] = -1;
+        at.bits = 0;
+        at.plain = false;
+        if (i >= mine) return at;
+        const int pos0 = first + i * (W * TILE), pos = pos0 + (g.page16 ? mine_at & 16 : mine_at);
+        const bool real_page = (uint32_t)page < (uint32_t)C.n_pages;
+        long long off = (page * C.page_stride +
+                         (long long)(pos - A::page_of(g, pos) * C.page_size) * C.token_stride) * S::ES;
+        if (g.page16 && D == DP && pos0 >= lo && pos0 + TILE <= t1 && __all_sync(~0u, real_page)) {
+          const long long own = (row0 * C.token_stride) * S::ES + ch * 16;
 #pragma unroll
-            for (int k = 0; k < kTile / RPI; ++k) {
-              put(k, ks, vs, true);
-              ks += step;
-              vs += step;
+          for (int mt = 0; mt < MT; ++mt) at.off[mt] = (MT == 1 ? off : __shfl_sync(~0u, off, 16 * mt)) + own;
+          at.bits = kAll;
+          at.plain = true;
+        } else {
+          const int me = pos0 + mine_at;
+          if (g.page16) off += (long long)(mine_at & 15) * C.token_stride * S::ES;
+          const bool seen = me >= lo && me < t1;
+          if (seen && !real_page) record_status(g.a.status, SPAX_ERR_INDEX);
+          at.off[0] = seen && real_page ? off : -1;
+          at.bits = __ballot_sync(~0u, at.off[0] >= 0) & kAll;
+        }
+        return at;
+      };
+      // Starts the copies of a tile's keys or values. Rows are 16-byte chunks, placed so that the
+      // fragments' loads spread over the banks: keys with rows of unlike parity in different halves,
+      // values with pairs of rows apart.
+      const long long step = RPI * C.token_stride * S::ES;
+      auto issue = [&](const Place& at, bool real_tile, bool keys, int slot) {
+        if (real_tile) {
+          const uint32_t piece = ring + slot * S::PIECE;
+          const uint8_t* pool = keys ? kpool : vpool;
+          auto spot = [&](int row_) {
+            const int to = S::CH >= 8 ? (keys ? ch ^ ((row_ & 1) << 2) : ch ^ (((row_ >> 1) & 3) << 1))
+                                      : (keys ? ch : ch ^ (((row_ >> 1) & 1) << 1));
+            return piece + row_ * S::ROW + to * 16;
+          };
+          if (at.plain) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const uint8_t* src = pool + at.off[mt];
+#pragma unroll
+              for (int k = 0; k < 16 / RPI; ++k) {
+                cp16(spot(mt * 16 + k * RPI + row0), src, true);
+                src += step;
+              }
             }
           } else {
-            const int pos = pos0 + (lane & 15);
-            long long off = -1;
-            if (pos >= lo && pos < t1) {
-              if ((uint32_t)page < (uint32_t)C.n_pages)
-                off = (page * C.page_stride +
-                       (long long)(pos - A::page_of(g, pos) * C.page_size) * C.token_stride) * S::ES;
-              else
-                record_status(g.a.status, SPAX_ERR_INDEX);
-            }
-            bits = __ballot_sync(~0u, off >= 0) & 0xFFFFu;
 #pragma unroll
-            for (int k = 0; k < kTile / RPI; ++k) {
-              const long long row_off = __shfl_sync(~0u, off, k * RPI + row0);
+            for (int k = 0; k < TILE / RPI; ++k) {
+              const long long row_off = __shfl_sync(~0u, at.off[0], k * RPI + row0);
               const bool real = row_off >= 0 && ch < chunks;
-              const long long at = real ? row_off + ch * 16 : 0;
-              put(k, kpool + at, vpool + at, real);
+              cp16(spot(k * RPI + row0), pool + (real ? row_off + ch * 16 : 0), real);
             }
           }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        return bits;
       };
+      auto next_slot = [](int slot) { return slot + 1 == S::SLOTS ? 0 : slot + 1; };
 
-      uint32_t seen[S::STAGES - 1];
-      int page = page_entry(0);
+      uint32_t seen[S::AHEAD];
+      int page = page_entry(0), fill = 0, use = 0;
 #pragma unroll
-      for (int i = 0; i < S::STAGES - 1; ++i) {
+      for (int i = 0; i < S::AHEAD; ++i) {
         const int next = page_entry(i + 1);
-        seen[i] = issue(i, page);
+        const Place at = place(i, page);
+        seen[i] = at.bits;
+        issue(at, i < mine, true, 2 * i);
+        issue(at, i < mine, false, 2 * i + 1);
         page = next;
       }
+      fill = 2 * S::AHEAD;
+      if constexpr (!CAREFUL) prepare_query();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         m[nt][0] = m[nt][1] = -INFINITY;
@@ -490,77 +578,109 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
         for (int i = 0; i < DP / 16; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
       }
       for (int i = 0; i < mine; ++i) {
-        const int next = page_entry(i + S::STAGES);
-        const uint32_t now = issue(i + S::STAGES - 1, page);
+        const int next = page_entry(i + S::AHEAD + 1);
+        const Place ahead = place(i + S::AHEAD, page);
         page = next;
         const uint32_t here = seen[0];
 #pragma unroll
-        for (int k = 0; k + 1 < S::STAGES - 1; ++k) seen[k] = seen[k + 1];
-        seen[S::STAGES - 2] = now;
-        asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 1) : "memory");
+        for (int k = 0; k + 1 < S::AHEAD; ++k) seen[k] = seen[k + 1];
+        seen[S::AHEAD - 1] = ahead.bits;
+        issue(ahead, i + S::AHEAD < mine, true, fill);
+        fill = next_slot(fill);
+        asm volatile("cp.async.wait_group %0;" ::"n"(S::SLOTS - 1) : "memory");
         __syncwarp();
-        const uint32_t ks_at = ring + (uint32_t)i % S::STAGES * S::STAGE, vs_at = ks_at + S::HALF;
+        const uint32_t ks_at = ring + use * S::PIECE;
+        use = next_slot(use);
 
         // scores: one chain for the first part of the query, one for the others
-        float acc[NT][2][4];
-        auto step = [&](int pair, const uint32_t(&a)[4], const uint32_t(&b)[4]) {
-          uint32_t fa[4], fb[4];
+        float acc[MT][NT][2][4];
+        auto step = [&](int pair, const uint32_t(&x)[MT][2][4]) {
+          uint32_t fin[MT][2][4];
           if constexpr (CAREFUL) {
-            finite_pairs(a, fa);
-            finite_pairs(b, fb);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              finite_pairs(x[mt][0], fin[mt][0]);
+              finite_pairs(x[mt][1], fin[mt][1]);
+            }
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int p = S::QP - 1; p >= 0; --p) {
               const uint4 v = lds128(qsm + ((pair * S::QP + p) * NT + nt) * 512 + lane * 16);
-              float(&d)[4] = acc[nt][p == 0 ? 0 : 1];
               const bool low = CAREFUL && p > 0;
-              if (pair == 0 && (p == 0 || p == S::QP - 1))
-                mma16816<S::E4M3, true>(d, low ? fa : a, v.x, v.y);
-              else
-                mma16816<S::E4M3, false>(d, low ? fa : a, v.x, v.y);
-              mma16816<S::E4M3, false>(d, low ? fb : b, v.z, v.w);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                float(&d)[4] = acc[mt][nt][p == 0 ? 0 : 1];
+                if (pair == 0 && (p == 0 || p == S::QP - 1))
+                  mma16816<S::E4M3, true>(d, low ? fin[mt][0] : x[mt][0], v.x, v.y);
+                else
+                  mma16816<S::E4M3, false>(d, low ? fin[mt][0] : x[mt][0], v.x, v.y);
+              }
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                mma16816<S::E4M3, false>(acc[mt][nt][p == 0 ? 0 : 1], low ? fin[mt][1] : x[mt][1], v.z, v.w);
             }
         };
 #pragma unroll
         for (int j = 0; j < S::CH / 4; ++j) {
           const int kc = S::CH >= 8 ? (c + 4 * j) ^ ((r & 1) << 2) : c + 4 * j;
-          const uint4 top = lds128(ks_at + r * S::ROW + kc * 16);
-          const uint4 low = lds128(ks_at + (r + 8) * S::ROW + kc * 16);
-          if constexpr (S::E4M3) {
-            const uint32_t tw[4] = {top.x, top.y, top.z, top.w}, lw[4] = {low.x, low.y, low.z, low.w};
-            uint32_t a[4][4];
+          uint4 top[MT], low[MT];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              e4m3x4_to_f16(tw[k], &a[k][0], &a[k][2]);
-              e4m3x4_to_f16(lw[k], &a[k][1], &a[k][3]);
+          for (int mt = 0; mt < MT; ++mt) {
+            top[mt] = lds128(ks_at + (mt * 16 + r) * S::ROW + kc * 16);
+            low[mt] = lds128(ks_at + (mt * 16 + r + 8) * S::ROW + kc * 16);
+          }
+          if constexpr (S::E4M3) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t x[MT][2][4];
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                e4m3x4_to_f16(k ? top[mt].z : top[mt].x, &x[mt][0][0], &x[mt][0][2]);
+                e4m3x4_to_f16(k ? low[mt].z : low[mt].x, &x[mt][0][1], &x[mt][0][3]);
+                e4m3x4_to_f16(k ? top[mt].w : top[mt].y, &x[mt][1][0], &x[mt][1][2]);
+                e4m3x4_to_f16(k ? low[mt].w : low[mt].y, &x[mt][1][1], &x[mt][1][3]);
+              }
+              step(2 * j + k, x);
             }
-            step(2 * j, a[0], a[1]);
-            step(2 * j + 1, a[2], a[3]);
           } else {
-            const uint32_t a0[4] = {top.x, low.x, top.y, low.y}, a1[4] = {top.z, low.z, top.w, low.w};
-            step(j, a0, a1);
+            uint32_t x[MT][2][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              x[mt][0][0] = top[mt].x, x[mt][0][1] = low[mt].x, x[mt][0][2] = top[mt].y, x[mt][0][3] = low[mt].y;
+              x[mt][1][0] = top[mt].z, x[mt][1][1] = low[mt].z, x[mt][1][2] = top[mt].w, x[mt][1][3] = low[mt].w;
+            }
+            step(j, x);
           }
         }
 
-        uint32_t pb[NT][S::PP][2];
+        uint32_t pb[MT][NT][S::PP][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float s[4];
+          float s[MT][4], n0 = m[nt][0], n1 = m[nt][1];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[k] = (acc[nt][1][k] + acc[nt][0][k]) * f1[nt][k & 1];
-          if (f2 > 0.0f) {
+          for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[k] = tanhf(s[k]) * f2;
+            for (int k = 0; k < 4; ++k) s[mt][k] = (acc[mt][nt][1][k] + acc[mt][nt][0][k]) * f1[nt][k & 1];
+            if (f2 > 0.0f) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) s[mt][k] = tanh_flat(s[mt][k]) * f2;
+            }
           }
-          if (here != 0xFFFFu) {
-            if (!(here >> r & 1)) s[0] = s[1] = -INFINITY;
-            if (!(here >> (r + 8) & 1)) s[2] = s[3] = -INFINITY;
+          if (here != kAll) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              if (!(here >> (mt * 16 + r) & 1)) s[mt][0] = s[mt][1] = -INFINITY;
+              if (!(here >> (mt * 16 + r + 8) & 1)) s[mt][2] = s[mt][3] = -INFINITY;
+            }
           }
-          const bool up = fmaxf(s[0], s[2]) > m[nt][0] + kSlack || fmaxf(s[1], s[3]) > m[nt][1] + kSlack;
-          if (__any_sync(~0u, up)) {
-            float n0 = fmaxf(m[nt][0], fmaxf(s[0], s[2])), n1 = fmaxf(m[nt][1], fmaxf(s[1], s[3]));
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            n0 = fmaxf(n0, fmaxf(s[mt][0], s[mt][2]));
+            n1 = fmaxf(n1, fmaxf(s[mt][1], s[mt][3]));
+          }
+          if (__any_sync(~0u, n0 > m[nt][0] + kSlack || n1 > m[nt][1] + kSlack)) {
 #pragma unroll
             for (int k = 4; k < 32; k <<= 1) {
               n0 = fmaxf(n0, __shfl_xor_sync(~0u, n0, k));
@@ -581,75 +701,92 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
               o[nt][k][3] *= f1_;
             }
           }
-          float p[4];
           const float base0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0] - kLift;
           const float base1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1] - kLift;
-          p[0] = exp2_ftz(s[0] - base0);
-          p[1] = exp2_ftz(s[1] - base1);
-          p[2] = exp2_ftz(s[2] - base0);
-          p[3] = exp2_ftz(s[3] - base1);
-          l[nt][0] += p[0] + p[2];
-          l[nt][1] += p[1] + p[3];
 #pragma unroll
-          for (int k = 0; k < S::PP; ++k) {
-            pb[nt][k][0] = transpose8x8(take_part<S::E4M3>(p[0], p[1]));
-            pb[nt][k][1] = transpose8x8(take_part<S::E4M3>(p[2], p[3]));
+          for (int mt = 0; mt < MT; ++mt) {
+            float p[4];
+            p[0] = exp2_ftz(s[mt][0] - base0);
+            p[1] = exp2_ftz(s[mt][1] - base1);
+            p[2] = exp2_ftz(s[mt][2] - base0);
+            p[3] = exp2_ftz(s[mt][3] - base1);
+            l[nt][0] += p[0] + p[2];
+            l[nt][1] += p[1] + p[3];
+#pragma unroll
+            for (int k = 0; k < S::PP; ++k) {
+              pb[mt][nt][k][0] = transpose8x8(take_part<S::E4M3>(p[0], p[1]));
+              pb[mt][nt][k][1] = transpose8x8(take_part<S::E4M3>(p[2], p[3]));
+            }
           }
         }
+
+        __syncwarp();  // every lane is done with the keys before their slot is filled again
+        issue(ahead, i + S::AHEAD < mine, false, fill);
+        fill = next_slot(fill);
+        asm volatile("cp.async.wait_group %0;" ::"n"(S::SLOTS - 1) : "memory");
+        __syncwarp();
+        const uint32_t vs_at = ring + use * S::PIECE;
+        use = next_slot(use);
 
         // outputs: 64 entries at a time; this lane's 8 are 64 j + 8 r + (0..7)
 #pragma unroll
         for (int j = 0; j < DP / 64; ++j) {
-          uint32_t w[4][4];  // [position 2c, 2c + 1, 2c + 8, 2c + 9][words of 8 entries]
+          uint32_t w[MT][4][4];  // [position 2c, 2c + 1, 2c + 8, 2c + 9][words of 8 entries]
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int row_ = 2 * c + (k & 1) + (k >> 1) * 8;
-            const int sw = S::CH >= 8 ? ((row_ >> 1) & 3) << 1 : ((row_ >> 1) & 1) << 1;
-            if constexpr (S::E4M3) {
-              const int unit = 8 * j + r;  // of 8 bytes
-              const uint2 v = lds64(vs_at + row_ * S::ROW + ((unit >> 1) ^ sw) * 16 + (unit & 1) * 8);
-              w[k][0] = v.x;
-              w[k][1] = v.y;
-            } else {
-              const uint4 v = lds128(vs_at + row_ * S::ROW + ((8 * j + r) ^ sw) * 16);
-              w[k][0] = v.x;
-              w[k][1] = v.y;
-              w[k][2] = v.z;
-              w[k][3] = v.w;
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row_ = mt * 16 + 2 * c + (k & 1) + (k >> 1) * 8;
+              const int sw = S::CH >= 8 ? ((row_ >> 1) & 3) << 1 : ((row_ >> 1) & 1) << 1;
+              if constexpr (S::E4M3) {
+                const int unit = 8 * j + r;  // of 8 bytes
+                const uint2 v = lds64(vs_at + row_ * S::ROW + ((unit >> 1) ^ sw) * 16 + (unit & 1) * 8);
+                w[mt][k][0] = v.x;
+                w[mt][k][1] = v.y;
+              } else {
+                const uint4 v = lds128(vs_at + row_ * S::ROW + ((8 * j + r) ^ sw) * 16);
+                w[mt][k][0] = v.x;
+                w[mt][k][1] = v.y;
+                w[mt][k][2] = v.z;
+                w[mt][k][3] = v.w;
+              }
             }
-          }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {  // entries 8 r + 2 q and 8 r + 2 q + 1
-            uint32_t a[4];
-            if constexpr (S::E4M3) {
-              const uint32_t sel = q & 1 ? 0x7362 : 0x5140;
-              e4m3x4_to_f16(__byte_perm(w[0][q / 2], w[1][q / 2], sel), &a[0], &a[1]);
-              e4m3x4_to_f16(__byte_perm(w[2][q / 2], w[3][q / 2], sel), &a[2], &a[3]);
-            } else {
-              a[0] = __byte_perm(w[0][q], w[1][q], 0x5410);
-              a[1] = __byte_perm(w[0][q], w[1][q], 0x7632);
-              a[2] = __byte_perm(w[2][q], w[3][q], 0x5410);
-              a[3] = __byte_perm(w[2][q], w[3][q], 0x7632);
+            uint32_t x[MT][4], fin[MT][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              if constexpr (S::E4M3) {
+                const uint32_t sel = q & 1 ? 0x7362 : 0x5140;
+                e4m3x4_to_f16(__byte_perm(w[mt][0][q / 2], w[mt][1][q / 2], sel), &x[mt][0], &x[mt][1]);
+                e4m3x4_to_f16(__byte_perm(w[mt][2][q / 2], w[mt][3][q / 2], sel), &x[mt][2], &x[mt][3]);
+              } else {
+                x[mt][0] = __byte_perm(w[mt][0][q], w[mt][1][q], 0x5410);
+                x[mt][1] = __byte_perm(w[mt][0][q], w[mt][1][q], 0x7632);
+                x[mt][2] = __byte_perm(w[mt][2][q], w[mt][3][q], 0x5410);
+                x[mt][3] = __byte_perm(w[mt][2][q], w[mt][3][q], 0x7632);
+              }
+              if constexpr (CAREFUL) finite_pairs(x[mt], fin[mt]);
             }
-            uint32_t fa[4];
-            if constexpr (CAREFUL) finite_pairs(a, fa);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float t[4];
 #pragma unroll
-              for (int k = S::PP - 1; k >= 0; --k) {
-                const bool low = CAREFUL && k > 0;
-                if (k == S::PP - 1)
-                  mma16816<S::E4M3, true>(t, low ? fa : a, pb[nt][k][0], pb[nt][k][1]);
-                else
-                  mma16816<S::E4M3, false>(t, low ? fa : a, pb[nt][k][0], pb[nt][k][1]);
-              }
+              for (int k = S::PP - 1; k >= 0; --k)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) o[nt][4 * j + q][k] += t[k];
+                for (int mt = 0; mt < MT; ++mt) {
+                  const uint32_t* a = CAREFUL && k > 0 ? fin[mt] : x[mt];
+                  if (k == S::PP - 1 && mt == 0)
+                    mma16816<S::E4M3, true>(t, a, pb[mt][nt][k][0], pb[mt][nt][k][1]);
+                  else
+                    mma16816<S::E4M3, false>(t, a, pb[mt][nt][k][0], pb[mt][nt][k][1]);
+                }
+#pragma unroll
+              for (int k = 0; k < 4; k += 2) add2(o[nt][4 * j + q][k], o[nt][4 * j + q][k + 1], t[k], t[k + 1]);
             }
           }
         }
-        __syncwarp();  // every lane is done with the stage before it is filled again
+        __syncwarp();
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     };
@@ -716,10 +853,10 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
 
     // ---- a shared row: the last CTA to arrive joins its parts ----------------------------------------
     if (!whole) {
-      const int b0 = (int)(((row_begin + 1) * B - 1) / U), b1 = (int)((row_end * B - 1) / U);
-      const int n = b1 - b0 + 1;
+      const int b0 = run ? (int)row_begin : (int)(((row_begin + 1) * B - 1) / U);
+      const int n = run ? runs : (int)(((row_begin + units) * B - 1) / U) - b0 + 1;
       // the first CTA's slot: its first segment if its run starts in this row
-      const int slot0 = 2 * b0 + (row_begin <= U * b0 / B ? 0 : 1);
+      const int slot0 = 2 * b0 + (run || row_begin <= U * b0 / B ? 0 : 1);
       const long long at = (long long)seq * g.a.n_heads + head0;
       auto slot_of = [&](int k) { return k == 0 ? slot0 : 2 * (b0 + k); };
       // In one step up to kJoin parts; else groups of about sqrt(n) first, each by its own last CTA,
@@ -730,15 +867,16 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       const int k0 = (b - b0) / group * group, groups = (n + group - 1) / group;
       bool last = arrive(g.tickets + slot_of(k0), min(group, n - k0), &is_last);
       if (last) {
-        join<S>(g, smem, heads, min(group, n - k0), [&](int i) { return slot_of(k0 + i); },
+        join<S>(g, heads, min(group, n - k0), [&](int i) { return slot_of(k0 + i); },
                 groups == 1 ? -1 : slot_of(k0), at);
         if (groups > 1) {
           last = arrive(g.tickets2 + slot0, groups, &is_last);
-          if (last) join<S>(g, smem, heads, groups, [&](int i) { return slot_of(i * group); }, -1, at);
+          if (last) join<S>(g, heads, groups, [&](int i) { return slot_of(i * group); }, -1, at);
         }
       }
     }
     __syncthreads();  // the join's buffer is read before the next segment fills the ring
+    if (run) break;
     x += u1 - u0;
     if (x == base + rows_of_seq * units) {
       base = x;
@@ -793,24 +931,36 @@ cudaError_t launch_paged_attention(const AttnLaunch& a, int sm_count, cudaStream
   while ((1ull << s) < d) ++s;
   g.page_shift = s - 1;
   g.page_mul = d == 1 ? 0 : (uint32_t)((1ull << (31 + s)) / d + 1);
-  g.page16 = d % kTile == 0;
+  g.page16 = d % 16 == 0;
   const int dp = padded_dim(a.cache.head_dim), nt = head_blocks(g.row_heads, a.cache.head_dim);
   const bool e = a.cache.dtype == SPAX_KV_E4M3;
-  // warps, stages and CTAs by what fits 227 KB and 65536 registers an SM
+  // warps, slots and CTAs by what fits 227 KB and 65536 registers an SM
+#ifndef CFG64E
+#define CFG64E 64, true, 1, 2, 4, 5, 3
+#define CFG64B 64, false, 1, 2, 4, 3, 3
+#define CFG128E 128, true, 1, 2, 4, 3, 3
+#define CFG128B 128, false, 1, 1, 4, 3, 3
+#define CFG256E 256, true, 1, 1, 4, 5, 2
+#define CFG256B 256, false, 1, 1, 4, 3, 2
+#define CFG64E2 64, true, 2, 1, 4, 7, 3
+#define CFG64B2 64, false, 2, 1, 4, 5, 3
+#define CFG128E2 128, true, 2, 1, 4, 7, 2
+#define CFG128B2 128, false, 2, 1, 4, 5, 2
+#endif
   if (dp == 64 && nt == 1)
-    return e ? launch_shape<AttnShape<64, true, 1, 4, 4, 4>>(g, sm_count, stream)
-             : launch_shape<AttnShape<64, false, 1, 4, 3, 4>>(g, sm_count, stream);
+    return e ? launch_shape<AttnShape<CFG64E>>(g, sm_count, stream)
+             : launch_shape<AttnShape<CFG64B>>(g, sm_count, stream);
   if (dp == 64)
-    return e ? launch_shape<AttnShape<64, true, 2, 4, 4, 3>>(g, sm_count, stream)
-             : launch_shape<AttnShape<64, false, 2, 4, 3, 3>>(g, sm_count, stream);
+    return e ? launch_shape<AttnShape<CFG64E2>>(g, sm_count, stream)
+             : launch_shape<AttnShape<CFG64B2>>(g, sm_count, stream);
   if (dp == 128 && nt == 1)
-    return e ? launch_shape<AttnShape<128, true, 1, 4, 4, 3>>(g, sm_count, stream)
-             : launch_shape<AttnShape<128, false, 1, 4, 2, 3>>(g, sm_count, stream);
+    return e ? launch_shape<AttnShape<CFG128E>>(g, sm_count, stream)
+             : launch_shape<AttnShape<CFG128B>>(g, sm_count, stream);
   if (dp == 128)
-    return e ? launch_shape<AttnShape<128, true, 2, 4, 4, 2>>(g, sm_count, stream)
-             : launch_shape<AttnShape<128, false, 2, 4, 3, 2>>(g, sm_count, stream);
-  return e ? launch_shape<AttnShape<256, true, 1, 4, 3, 2>>(g, sm_count, stream)
-           : launch_shape<AttnShape<256, false, 1, 6, 2, 1>>(g, sm_count, stream);
+    return e ? launch_shape<AttnShape<CFG128E2>>(g, sm_count, stream)
+             : launch_shape<AttnShape<CFG128B2>>(g, sm_count, stream);
+  return e ? launch_shape<AttnShape<CFG256E>>(g, sm_count, stream)
+           : launch_shape<AttnShape<CFG256B>>(g, sm_count, stream);
 }
 
 }  // namespace spax
