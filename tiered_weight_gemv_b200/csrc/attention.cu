@@ -54,6 +54,9 @@ struct AttnShape {
   static constexpr int RING = WARPS * SLOTS * PIECE;
   static_assert(SLOTS % 2 == 1 && SLOTS >= 3);
   static constexpr int KS = DP / 16;              // k steps of a score
+  // Units of the dealing that a row counts for beside its own: the start-up and the end of a segment
+  // take about as long as the copies of 64 KB at a CTA's share of the bandwidth.
+  static constexpr int EXTRA = 512 / ROW > 1 ? 512 / ROW : 1;
   static constexpr int SMEM = RING + KS / 2 * QP * NT * 512;  // and the query's parts
   static constexpr int OS = DP + 4;               // row stride of the warps' outputs at the join
   static_assert(WARPS * HB * OS * 4 <= RING, "the join's buffer overlays the ring");
@@ -301,8 +304,9 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
     for (int w = 0; w < W; ++w) x += prefix[w];
     return x;
   };
-  const long long U = rows_of_seq * total([](int u) { return u; });
+  long long U = rows_of_seq * total([](int u) { return u; });
   long long B = min((long long)gridDim.x, U);
+  int extra = 0;
   int run = 0;  // units in a run of the first kind
   if (U > 0) {
     const long long rows = rows_of_seq * total([](int u) { return u > 0; });
@@ -322,6 +326,10 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
           break;
         }
       }
+    }
+    if (!run) {
+      extra = S::EXTRA;
+      U += rows * extra;
     }
   }
   if (b == 0) {
@@ -346,7 +354,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
   const long long begin = run ? b : U * b / B, end = run ? b + 1 : U * (b + 1) / B;
   auto weight = [&](int s) {
     const int u = units_at(s);
-    return rows_of_seq * (run ? (u + run - 1) / run : u);
+    return rows_of_seq * (run ? (u + run - 1) / run : u ? u + extra : 0);
   };
   int seq;
   long long base;
@@ -396,11 +404,12 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       continue;
     }
     const long long y = x - base;
-    const int runs = run ? (units + run - 1) / run : units;  // the coordinate's extent of a row
+    const int runs = run ? (units + run - 1) / run : units + extra;  // what the row counts for
     const int row = (int)(y / runs), r0 = (int)(y - (long long)row * runs);
-    const int u0 = run ? r0 * run : r0;
-    const int u1 = (int)min((long long)units, u0 + (run ? run : end - x));
-    const long long row_begin = base + (long long)row * runs;
+    const int u0 = run ? r0 * run : max(0, r0 - extra);
+    const int u1 = run ? min(units, u0 + run) : (int)min((long long)units, r0 - extra + (end - x));
+    const long long row_begin = base + (long long)row * runs + extra;  // the first unit's place
+    if (u1 <= u0) break;  // the run ends before the row's first unit
     const int kvh = row / g.blocks, hb = row - kvh * g.blocks;
     const int heads = min(HB, g.row_heads - hb * HB);   // real query heads of this block
     const int head0 = kvh * g.row_heads + hb * HB;
@@ -877,8 +886,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
     }
     __syncthreads();  // the join's buffer is read before the next segment fills the ring
     if (run) break;
-    x += u1 - u0;
-    if (x == base + rows_of_seq * units) {
+    x += runs - r0;
+    if (x == base + rows_of_seq * runs) {
       base = x;
       ++seq;
     }
