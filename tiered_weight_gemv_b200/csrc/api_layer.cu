@@ -63,8 +63,8 @@ spax_status spax_kv_append(const spax_kv_cache* h_cache, const float* q, int64_t
   AppendLaunch a = {};
   const spax_status st = check_cache(h_cache, &a.cache);
   if (st != SPAX_OK) return st;
-  if (n_tok < 0 || n_seq < 0 || n_heads < 0 || n_heads > (1 << 20)) return SPAX_ERR_SHAPE;
-  if (a.cache.n_kv_heads > (1 << 20)) return SPAX_ERR_SHAPE;
+  if (n_tok < 0 || n_seq < 0 || n_heads < 0 || n_heads > 65536) return SPAX_ERR_SHAPE;
+  if (a.cache.n_kv_heads > 65536) return SPAX_ERR_SHAPE;
   if ((n_heads == 0) != (q == nullptr)) return SPAX_ERR_ARG;
   if (n_tok == 0) return SPAX_OK;
   if (!pos || !page_table || n_seq < 1) return SPAX_ERR_ARG;
@@ -99,7 +99,9 @@ spax_status spax_kv_append(const spax_kv_cache* h_cache, const float* q, int64_t
   a.n_heads = n_heads;
   a.n_seq = n_seq;
   a.max_pages = max_pages;
-  return launch_status(launch_kv_append(a, static_cast<cudaStream_t>(stream)));
+  const int sms = sm_count_current_device();
+  if (sms < 1) return SPAX_ERR_CUDA;
+  return launch_status(launch_kv_append(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t spax_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim) {
@@ -196,7 +198,9 @@ spax_status spax_residual_norm(const float* h, const float* y, int n_tok, int d,
   a.out_scale = out_scale;
   a.n_tok = n_tok;
   a.d = d;
-  return launch_status(launch_residual_norm(a, static_cast<cudaStream_t>(stream)));
+  const int sms = sm_count_current_device();
+  if (sms < 1) return SPAX_ERR_CUDA;
+  return launch_status(launch_residual_norm(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

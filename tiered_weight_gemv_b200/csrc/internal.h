@@ -79,7 +79,7 @@ struct AppendLaunch {
   int32_t* status;
   int n_tok, n_heads, n_seq, max_pages;
 };
-cudaError_t launch_kv_append(const AppendLaunch& a, cudaStream_t stream);
+cudaError_t launch_kv_append(const AppendLaunch& a, int sm_count, cudaStream_t stream);
 
 struct AttnLaunch {
   spax_kv_cache cache;
@@ -104,7 +104,7 @@ struct NormLaunch {
   float res_scale, out_scale;
   int n_tok, d;
 };
-cudaError_t launch_residual_norm(const NormLaunch& a, cudaStream_t stream);
+cudaError_t launch_residual_norm(const NormLaunch& a, int sm_count, cudaStream_t stream);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -473,37 +473,48 @@ def alloc_workspace(op: int, d_out: int, d_in: int, device="cuda") -> torch.Tens
 
 # ------------------------------------------------------------- the decode layer between projections
 
-def _on(dev: int, t, dtype, name: str) -> int:
-    """The address of a tensor of the call's device (None: a null pointer); rows may be strided."""
-    if t is None:
-        return 0
+# These calls stand between kernels of a few microseconds, so their argument checks are kept short:
+# one look at each tensor's type, device and address, and the stream's handle without its object.
+_f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
+_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _refuse(t, dtype, dev: int, name: str):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def _on(t, dtype, dev: int, name: str) -> int:
+    """The address of a tensor of the current device; rows may be strided."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, dtype, dev, name)
     return t.data_ptr()
 
 
-def _whole(dev: int, t, dtype, name: str) -> int:
-    if t is not None and isinstance(t, torch.Tensor) and not t.is_contiguous():
+def _whole(t, dtype, dev: int, name: str):
+    """The address of a contiguous tensor of the current device (None: a null pointer)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, dtype, dev, name)
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return _on(dev, t, dtype, name)
+    return t.data_ptr()
 
 
-def _raw_stream(stream, dev: int) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
-
-
-def _heads(t: torch.Tensor, name: str):
-    """[tokens, heads, head_dim] whose heads are contiguous; the tokens' stride is free."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    n, h, d = t.shape
-    if t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+def _heads(t: torch.Tensor, d: int, name: str):
+    """(tokens, heads, the tokens' stride) of [tokens, heads, d] whose heads are contiguous."""
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError(f"{name} must be [tokens, heads, {d}]")
+    stride = t.stride()
+    if stride[2] != 1 or (stride[1] != d and shape[1] > 1 and shape[0] > 0):
         raise ValueError(f"{name}'s heads must be contiguous within a token")
-    return n, h, t.stride(0)
+    return shape[0], shape[1], stride[0]
 
 
 class KvCache:
@@ -523,7 +534,7 @@ class KvCache:
                              "with the same strides, the last of them 1")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = k.shape
-        self.dtype, self.device = kinds[k.dtype], k.device
+        self.dtype, self.device, self._dev = kinds[k.dtype], k.device, k.get_device()
         self._desc = spax_kv_cache(*k.shape, self.dtype, k_scale, v_scale, 0, *k.stride()[:3],
                                    k.data_ptr(), v.data_ptr())
         self._ref = ctypes.byref(self._desc)
@@ -552,8 +563,9 @@ class Rope:
 
     def __init__(self, inv_freq: torch.Tensor, interleaved: bool = False):
         dev = inv_freq.get_device() if inv_freq.is_cuda else -1
-        ptr = _whole(dev, inv_freq, torch.float64, "inv_freq")
-        self.inv_freq, self.interleaved = inv_freq, bool(interleaved)
+        ptr = _whole(inv_freq, torch.float64, dev, "inv_freq") if dev >= 0 else _refuse(
+            inv_freq, torch.float64, dev, "inv_freq")
+        self.inv_freq, self.interleaved, self._dev = inv_freq, bool(interleaved), dev
         self._desc = spax_rope(2 * inv_freq.numel(), int(self.interleaved), ptr)
         self._ref = ctypes.byref(self._desc)
 
@@ -573,8 +585,9 @@ class Norm:
         self.d = given[0].numel() if given else None
         self.device = given[0].get_device() if given else None
         dt = types.pop()
-        ptrs = [_whole(self.device, t, dt, n) if t is not None else 0
-                for t, n in ((weight, "weight"), (bias, "bias"))]
+        ptrs = [_whole(t, dt, self.device, n) for t, n in ((weight, "weight"), (bias, "bias"))]
+        if self.device == -1:
+            raise TypeError("weight and bias must be CUDA tensors")
         self._desc = spax_norm(kind, int(dt == torch.bfloat16), *ptrs, eps)
         self._ref = ctypes.byref(self._desc)
 
@@ -585,10 +598,11 @@ class Norm:
         return self._ref
 
 
-def _table(t: torch.Tensor, n_seq: int):
-    if t.dim() != 2 or t.shape[0] < n_seq:
-        raise ValueError("page_table must be [sequences, pages]")
-    return t.shape
+def _at_home(obj, dev: int, name: str):
+    """The descriptor of an object whose tensors are on the current device."""
+    if obj._dev != dev:
+        raise ValueError(f"the {name} is on cuda:{obj._dev}, the current device is cuda:{dev}")
+    return obj._ref
 
 
 def spax_kv_append(cache: KvCache, q, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
@@ -598,40 +612,36 @@ def spax_kv_append(cache: KvCache, q, k: torch.Tensor, v: torch.Tensor, pos: tor
     [tokens, n_kv_heads, head_dim], fp32, the tokens' strides free (parts of one qkv row); q None:
     keys and values alone. q_out None: q is rotated in place. pos, seq int32 [tokens] (seq None:
     token t is of sequence t), page_table int32 [sequences, pages]; pos < 0 marks padding."""
-    dev = torch.cuda.current_device()
-    f32, i32 = torch.float32, torch.int32
-    n, kh, ks = _heads(k, "k")
-    nv, vh, vs = _heads(v, "v")
-    H = qs = os_ = 0
+    dev, d, heads_kv = _device(), cache.head_dim, cache.n_kv_heads
+    n, kh, ks = _heads(k, d, "k")
+    nv, vh, vs = _heads(v, d, "v")
+    nq, heads, qs, os_, qp, op = n, 0, 0, 0, None, None
     if q is not None:
-        nq, H, qs = _heads(q, "q")
+        nq, heads, qs = _heads(q, d, "q")
+        qp = _on(q, _f32, dev, "q")
         if q_out is None:
-            q_out = q
-        if q_out.shape != q.shape or nq != n or q.shape[2] != cache.head_dim:
-            raise ValueError("q / q_out sizes do not match k or the cache")
-        os_ = _heads(q_out, "q_out")[2]
+            os_, op = qs, qp
+        else:
+            if q_out.shape != q.shape:
+                raise ValueError("q_out's size does not match q")
+            os_, op = _heads(q_out, d, "q_out")[2], _on(q_out, _f32, dev, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if (nv != n or kh != cache.n_kv_heads or vh != kh or k.shape[2] != cache.head_dim
-            or v.shape[2] != cache.head_dim or pos.numel() != n
+    if (nq != n or nv != n or kh != heads_kv or vh != heads_kv or pos.numel() != n
             or (seq is not None and seq.numel() != n)):
-        raise ValueError("k / v / pos / seq sizes do not match the cache or one another")
-    n_seq, max_pages = _table(page_table, n if seq is None else 0)
+        raise ValueError("q / k / v / pos / seq sizes do not match the cache or one another")
+    n_seq, max_pages = page_table.shape
+    if seq is None and n_seq < n:
+        raise ValueError("page_table has fewer rows than there are tokens")
     st = _lib.spax_kv_append(
-        cache._ref if cache.device.index == dev else _on(dev, cache.k, cache.k.dtype, "cache"),
-        _on(dev, q, f32, "q"), qs, _on(dev, k, f32, "k"), ks, _on(dev, v, f32, "v"), vs, n, H,
-        _whole(dev, seq, i32, "seq"), _whole(dev, pos, i32, "pos"),
-        _whole(dev, page_table, i32, "page_table"), n_seq, max_pages,
-        None if rope is None else _rope_on(rope, dev), _on(dev, q_out, f32, "q_out"), os_,
-        _whole(dev, status, i32, "status"), _raw_stream(stream, dev))
+        _at_home(cache, dev, "cache"), qp, qs, _on(k, _f32, dev, "k"), ks, _on(v, _f32, dev, "v"),
+        vs, n, heads, _whole(seq, _i32, dev, "seq"), _whole(pos, _i32, dev, "pos"),
+        _whole(page_table, _i32, dev, "page_table"), n_seq, max_pages,
+        None if rope is None else _at_home(rope, dev, "rope"), op, os_,
+        _whole(status, _i32, dev, "status"),
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise SpaxError("spax_kv_append", st)
-
-
-def _rope_on(rope: Rope, dev: int):
-    if rope.inv_freq.get_device() != dev:
-        _on(dev, rope.inv_freq, torch.float64, "inv_freq")
-    return rope._ref
 
 
 def spax_attention_workspace_bytes(n_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -654,21 +664,23 @@ def spax_paged_attention(cache: KvCache, q: torch.Tensor, page_table: torch.Tens
     """Attention of one new token of each sequence over the cache: q fp32 [sequences, heads,
     head_dim] (the sequences' stride free), seq_lens int32 [sequences] counting the new token, out
     fp32 as q, contiguous; lse (optional) fp32 [sequences, heads]."""
-    dev = torch.cuda.current_device()
-    f32, i32 = torch.float32, torch.int32
-    n, H, qs = _heads(q, "q")
-    if q.shape[2] != cache.head_dim or out.shape != q.shape or seq_lens.numel() != n:
-        raise ValueError("q / out / seq_lens sizes do not match the cache or one another")
-    if lse is not None and lse.numel() != n * H:
+    dev = _device()
+    n, heads, qs = _heads(q, cache.head_dim, "q")
+    if out.shape != q.shape or seq_lens.numel() != n:
+        raise ValueError("q / out / seq_lens sizes do not match one another")
+    if lse is not None and lse.numel() != n * heads:
         raise ValueError("lse must be [sequences, heads]")
-    max_pages = _table(page_table, n)[1]
-    prm = spax_attn_params(scale, softcap, window)
+    n_seq, max_pages = page_table.shape
+    if n_seq < n:
+        raise ValueError("page_table has fewer rows than there are sequences")
     st = _lib.spax_paged_attention(
-        cache._ref if cache.device.index == dev else _on(dev, cache.k, cache.k.dtype, "cache"),
-        _on(dev, q, f32, "q"), qs, n, H, _whole(dev, page_table, i32, "page_table"), max_pages,
-        _whole(dev, seq_lens, i32, "seq_lens"), ctypes.byref(prm), _whole(dev, out, f32, "out"),
-        _whole(dev, lse, f32, "lse"), _whole(dev, status, i32, "status"),
-        _whole(dev, ws, torch.uint8, "ws"), ws.numel(), _raw_stream(stream, dev))
+        _at_home(cache, dev, "cache"), _on(q, _f32, dev, "q"), qs, n, heads,
+        _whole(page_table, _i32, dev, "page_table"), max_pages,
+        _whole(seq_lens, _i32, dev, "seq_lens"),
+        ctypes.byref(spax_attn_params(scale, softcap, window)), _whole(out, _f32, dev, "out"),
+        _whole(lse, _f32, dev, "lse"), _whole(status, _i32, dev, "status"),
+        _whole(ws, _u8, dev, "ws"), ws.numel(),
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise SpaxError("spax_paged_attention", st)
 
@@ -678,24 +690,25 @@ def spax_residual_norm(h: torch.Tensor, y, r, x, pre=None, post=None, gate=None,
     """r = res_scale h + out_scale gate N_post(y), x = N_pre(r) by rows: h, y, r, x fp32
     [..., d] of the same size (y None: r = res_scale h; r or x None: not written; r and x may be h
     or y), gate fp32 [d] for all rows or one row each, pre and post a Norm or None."""
-    dev = torch.cuda.current_device()
-    f32 = torch.float32
-    d = h.shape[-1] if h.dim() else 0
+    dev = _device()
+    shape = h.shape
+    d = shape[-1] if len(shape) else 0
     if d == 0:
         raise ValueError("rows must have entries")
     n = h.numel() // d
-    for t, name in ((y, "y"), (r, "r"), (x, "x")):
-        if t is not None and t.shape != h.shape:
-            raise ValueError(f"{name}'s size does not match h")
+    if ((y is not None and y.shape != shape) or (r is not None and r.shape != shape)
+            or (x is not None and x.shape != shape)):
+        raise ValueError("h / y / r / x sizes do not match")
     gs = 0
     if gate is not None:
         if gate.shape[-1] != d or gate.numel() not in (d, n * d):
             raise ValueError("gate must be [d] or of h's size")
         gs = d if gate.numel() == n * d and gate.dim() > 1 else 0
     st = _lib.spax_residual_norm(
-        _whole(dev, h, f32, "h"), _whole(dev, y, f32, "y"), n, d,
-        None if post is None else post._for(d, dev), _whole(dev, gate, f32, "gate"), gs, res_scale,
-        out_scale, None if pre is None else pre._for(d, dev), _whole(dev, r, f32, "r"),
-        _whole(dev, x, f32, "x"), _raw_stream(stream, dev))
+        _whole(h, _f32, dev, "h"), _whole(y, _f32, dev, "y"), n, d,
+        None if post is None else post._for(d, dev), _whole(gate, _f32, dev, "gate"), gs,
+        res_scale, out_scale, None if pre is None else pre._for(d, dev),
+        _whole(r, _f32, dev, "r"), _whole(x, _f32, dev, "x"),
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise SpaxError("spax_residual_norm", st)
