@@ -522,8 +522,8 @@ typedef struct {
  * [0, n_pages) does the same and sets *d_status = SPAX_ERR_INDEX. The tokens' (page, row) places in
  * one call must differ; where two agree, that row's contents are unspecified.
  * Requires h_rope (NULL: no rotation) as above; d_q, d_k, d_v, d_q_out 16-byte aligned, strides
- * multiples of 4 and at least the row when n_tok > 1; n_tok >= 0 (0: nothing is done); max_pages *
- * page_size < 2^31. No workspace.
+ * multiples of 4 and at least the row when n_tok > 1; n_tok >= 0 (0: nothing is done); at most 65536
+ * heads of each kind; max_pages * page_size < 2^31. No workspace.
  */
 spax_status spax_kv_append(const spax_kv_cache* h_cache, const float* d_q, int64_t q_stride,
                            const float* d_k, int64_t k_stride, const float* d_v, int64_t v_stride,
@@ -562,7 +562,8 @@ typedef struct {
  * must not run concurrently. No CTA waits for another.
  * Requires n_heads a multiple of n_kv_heads, q_stride a multiple of 4 and at least n_heads *
  * head_dim when n_seq > 1, d_q and d_out 16-byte aligned and not overlapping, n_seq >= 0 (0: nothing
- * is done), max_pages * page_size < 2^31.
+ * is done, at most 65535), max_pages * page_size < 2^31 and n_seq * n_kv_heads * ceil(n_heads /
+ * n_kv_heads / 8) * (max_pages * page_size / 64 + 10) < 2^31.
  */
 spax_status spax_paged_attention(const spax_kv_cache* h_cache, const float* d_q, int64_t q_stride,
                                  int n_seq, int n_heads, const int32_t* d_page_table,

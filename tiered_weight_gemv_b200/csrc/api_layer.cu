@@ -133,6 +133,10 @@ spax_status spax_paged_attention(const spax_kv_cache* h_cache, const float* q, i
   if (!rows_ok(q, q_stride, width, n_seq)) return SPAX_ERR_ARG;
   if (overlap(q, (n_seq - 1) * (n_seq > 1 ? q_stride : 0) + width, out, n_seq * width))
     return SPAX_ERR_ARG;
+  // the kernel counts units of 64 positions of all rows, and up to 8 more for each row, in 32 bits
+  const long long row_units = ((long long)max_pages * a.cache.page_size + 63) / 64 + 1 + 8;
+  const long long rows = (long long)a.cache.n_kv_heads * ((n_heads / a.cache.n_kv_heads + 7) / 8);
+  if (row_units * rows * n_seq >= INT_MAX) return SPAX_ERR_SHAPE;
   const int sms = sm_count_current_device();
   if (sms < 1) return SPAX_ERR_CUDA;
   if (!ws || ws_bytes < attention_ws_bytes(n_heads, a.cache.n_kv_heads, a.cache.head_dim, sms))

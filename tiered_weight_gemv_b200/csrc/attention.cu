@@ -219,10 +219,9 @@ __device__ __forceinline__ void put_row(const AttnArgs& g, int slot, long long a
 }
 
 // Joins n parts of a row, the slots of which slot_of gives, in their order: a thread takes the
-// maxima, sums and entries of eight parts at a time, all in flight at once.
-template <class S, class F>
+// maxima, sums and entries of N parts at a time, all in flight at once.
+template <class S, int N, class F>
 __device__ __forceinline__ void join(const AttnArgs& g, int heads, int n, F slot_of, int to, long long at) {
-  constexpr int N = 8;
   const int quads = g.a.cache.head_dim / 4;
   for (int e = threadIdx.x; e < heads * quads; e += S::THREADS) {
     const int h = e / quads, d = (e - h * quads) * 4;
@@ -233,22 +232,22 @@ __device__ __forceinline__ void join(const AttnArgs& g, int heads, int n, F slot
       float2 ml[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const long long slot = slot_of(min(k + i, n - 1));
-        ml[i] = __ldcg(g.part_ml + slot * S::HB + h);
-        t[i] = __ldcg(reinterpret_cast<const float4*>(g.part + (slot * S::HB + h) * S::DP + d));
+        ml[i] = make_float2(-INFINITY, 0.0f);
+        t[i] = make_float4(0, 0, 0, 0);
+        if (k + i < n) {
+          const long long slot = slot_of(k + i);
+          ml[i] = __ldcg(g.part_ml + slot * S::HB + h);
+          t[i] = __ldcg(reinterpret_cast<const float4*>(g.part + (slot * S::HB + h) * S::DP + d));
+        }
       }
       float top = M;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (k + i >= n) ml[i] = make_float2(-INFINITY, 0.0f);
-        top = fmaxf(top, ml[i].x);  // drops a NaN: its sum is NaN too
-      }
-      const float fade = M == -INFINITY ? (L == 0.0f ? 0.0f : L) : exp2_ftz(M - top);  // L may be NaN
+      for (int i = 0; i < N; ++i) top = fmaxf(top, ml[i].x);  // drops a NaN: its sum is NaN too
+      const float fade = M == -INFINITY ? 0.0f : exp2_ftz(M - top);
       L *= fade;
       v.x *= fade, v.y *= fade, v.z *= fade, v.w *= fade;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (ml[i].x == -INFINITY && ml[i].y == 0.0f) continue;  // nothing seen
         const float f = ml[i].x == -INFINITY ? 0.0f : exp2_ftz(ml[i].x - top);
         L += f * ml[i].y;
         v.x += f * t[i].x, v.y += f * t[i].y, v.z += f * t[i].z, v.w += f * t[i].w;
@@ -258,13 +257,18 @@ __device__ __forceinline__ void join(const AttnArgs& g, int heads, int n, F slot
     put_row<S>(g, to, at, h, d, v, M, L);
   }
 }
+template <class S, class F>
+__device__ __forceinline__ void join(const AttnArgs& g, int heads, int n, F slot_of, int to, long long at) {
+  if (n <= 4)
+    join<S, 4>(g, heads, n, slot_of, to, at);
+  else
+    join<S, 16>(g, heads, n, slot_of, to, at);
+}
 
 template <class S>
 __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const AttnArgs g) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long prefix[S::WARPS];
-  __shared__ long long start_base;
-  __shared__ int start_seq;
+  __shared__ int prefix[S::WARPS], start_base, start_seq;
   __shared__ float2 warp_ml[S::WARPS][S::HB];
   __shared__ bool is_last;
   using A = Attn<S>;
@@ -277,7 +281,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
   const spax_kv_cache& C = g.a.cache;
   const int D = C.head_dim, n_seq = g.a.n_seq;
   const int chunks = D * S::ES / 16;
-  const long long rows_of_seq = (long long)C.n_kv_heads * g.blocks;
+  const int rows_of_seq = C.n_kv_heads * g.blocks;
 
   pdl_wait();
   pdl_launch_dependents();
@@ -286,38 +290,40 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
   // Where a run length gives every row whole CTAs of its own within the wave (runs start at row
   // starts, the last of a row may be shorter), that is taken: one segment, one start-up and one
   // join for each CTA. Else all units are dealt in equal runs across row ends.
-  auto units_at = [&](int s) {
+  auto len_at = [&](int s) {
     bool bad;
-    return s < n_seq ? A::units_of(g, A::clipped_len(g, s, &bad)) : 0;
+    return s < n_seq ? A::clipped_len(g, s, &bad) : 0;
   };
   const bool few = n_seq <= 32;  // a lane for each sequence, and no barriers
   const int per = few ? 1 : (n_seq + T - 1) / T, s0 = few ? lane : tid * per;
-  auto total = [&](auto f) -> long long {  // sum of f(units) over the sequences
-    if (few) return __reduce_add_sync(~0u, (unsigned)f(units_at(lane)));
-    long long x = 0;
+  const int own_len = few ? len_at(lane) : 0, own_units = A::units_of(g, own_len);
+  auto units_at = [&](int s) { return A::units_of(g, len_at(s)); };
+  auto total = [&](auto f) -> int {  // sum of f(units) over the sequences
+    if (few) return (int)__reduce_add_sync(~0u, (unsigned)f(own_units));
+    unsigned x = 0;
     for (int k = 0; k < per; ++k) x += f(units_at(s0 + k));
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    x = __reduce_add_sync(~0u, x);
     __syncthreads();
-    if (lane == 0) prefix[warp] = x;
+    if (lane == 0) prefix[warp] = (int)x;
     __syncthreads();
-    x = 0;
-    for (int w = 0; w < W; ++w) x += prefix[w];
-    return x;
+    int all = 0;
+    for (int w = 0; w < W; ++w) all += prefix[w];
+    return all;
   };
-  long long U = rows_of_seq * total([](int u) { return u; });
-  long long B = min((long long)gridDim.x, U);
+  int U = rows_of_seq * total([](int u) { return u; });
+  int B = min((int)gridDim.x, U);
   int extra = 0;
   int run = 0;  // units in a run of the first kind
   if (U > 0) {
-    const long long rows = rows_of_seq * total([](int u) { return u > 0; });
-    if (2 * rows <= gridDim.x) {
-      run = (int)((U + B - 1) / B);
+    const int rows = rows_of_seq * total([](int u) { return u > 0; });
+    if (2 * rows <= (int)gridDim.x) {
+      run = (U + B - 1) / B;
       // a run may be this much longer than equal runs before their row ends cost less
       const int most = run + max(6, run / 8);
       const int more = few ? max(1, run / 16) : (most - run) / 2;
       for (;; run += more) {
-        const long long n = rows_of_seq * total([run](int u) { return (u + run - 1) / run; });
-        if (n <= gridDim.x) {
+        const int n = rows_of_seq * total([run](int u) { return (u + run - 1) / run; });
+        if (n <= (int)gridDim.x) {
           B = n;
           break;
         }
@@ -332,54 +338,57 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       U += rows * extra;
     }
   }
-  if (b == 0) {
-    bool any_bad = false;
-    for (int k = tid; k < n_seq; k += T) {
-      bool bad;
-      A::clipped_len(g, k, &bad);
-      any_bad |= bad;
+  // Rows that see nothing, and lengths to report: after this CTA's share.
+  auto leftovers = [&] {
+    if (b == 0) {
+      bool any_bad = false;
+      for (int k = tid; k < n_seq; k += T) {
+        bool bad;
+        A::clipped_len(g, k, &bad);
+        any_bad |= bad;
+      }
+      if (any_bad) record_status(g.a.status, SPAX_ERR_INDEX);
     }
-    if (any_bad) record_status(g.a.status, SPAX_ERR_INDEX);
-  }
-  // rows that see nothing
-  for (int s = b; s < n_seq; s += gridDim.x) {
-    if (units_at(s) != 0) continue;
-    for (int i = tid; i < g.a.n_heads * D; i += T) g.a.out[(long long)s * g.a.n_heads * D + i] = 0.0f;
-    if (g.a.lse)
-      for (int i = tid; i < g.a.n_heads; i += T) g.a.lse[(long long)s * g.a.n_heads + i] = -INFINITY;
-  }
-  if (b >= B) return;
-
-  // the sequence of the share's first unit (run), and the units (runs) before it
-  const long long begin = run ? b : U * b / B, end = run ? b + 1 : U * (b + 1) / B;
-  auto weight = [&](int s) {
-    const int u = units_at(s);
-    return rows_of_seq * (run ? (u + run - 1) / run : u ? u + extra : 0);
+    for (int s = b; s < n_seq; s += gridDim.x) {
+      if (units_at(s) != 0) continue;
+      for (int i = tid; i < g.a.n_heads * D; i += T) g.a.out[(long long)s * g.a.n_heads * D + i] = 0.0f;
+      if (g.a.lse)
+        for (int i = tid; i < g.a.n_heads; i += T) g.a.lse[(long long)s * g.a.n_heads + i] = -INFINITY;
+    }
   };
-  int seq;
-  long long base;
+  if (b >= B) {
+    leftovers();
+    return;
+  }
+
+  // CTA k's share is [start_of(k), start_of(k + 1)) of the units, floor(U k / B), or run k; the
+  // sequence of its first unit (run), and the units (runs) before that sequence
+  auto start_of = [&](int k) { return run ? k : U / B * k + U % B * k / B; };
+  const int begin = start_of(b), end = start_of(b + 1);
+  auto weight = [&](int u) { return rows_of_seq * (run ? (u + run - 1) / run : u ? u + extra : 0); };
+  int seq, base, len = 0;
   {
-    const long long own = weight(s0);
-    long long sum = own;
-    for (int k = 1; k < per; ++k) sum += weight(s0 + k);
-    long long x = sum;  // inclusive scan
+    const int own = weight(few ? own_units : units_at(s0));
+    int sum = own;
+    for (int k = 1; k < per; ++k) sum += weight(units_at(s0 + k));
+    int x = sum;  // inclusive scan
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(~0u, x, o);
+      const int y = __shfl_up_sync(~0u, x, o);
       if (lane >= o) x += y;
     }
     if (few) {
       seq = __popc(__ballot_sync(~0u, x <= begin));
       base = __shfl_sync(~0u, x - own, seq);
+      len = __shfl_sync(~0u, own_len, seq);
     } else {
       __syncthreads();
       if (lane == 31) prefix[warp] = x;
       __syncthreads();
       for (int w = 0; w < warp; ++w) x += prefix[w];
       if (x - sum <= begin && begin < x) {
-        long long at = x - sum;
-        int s = s0;
+        int at = x - sum, s = s0;
         for (;; ++s) {
-          const long long n = weight(s);
+          const int n = weight(units_at(s));
           if (begin < at + n) break;
           at += n;
         }
@@ -389,27 +398,26 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       __syncthreads();
       seq = start_seq;
       base = start_base;
+      len = len_at(seq);
     }
   }
 
   const uint32_t ring = smem_u32(smem) + warp * (S::SLOTS * S::PIECE);
   const uint32_t qsm = smem_u32(smem) + S::RING;
 
-  for (long long x = begin; x < end;) {
-    bool bad;
-    const int len = A::clipped_len(g, seq, &bad);
+  for (int x = begin; x < end;) {
     const int units = A::units_of(g, len);
     if (units == 0) {  // an empty sequence between two others
-      ++seq;
+      len = len_at(++seq);
       continue;
     }
-    const long long y = x - base;
+    const int y = x - base;
     const int runs = run ? (units + run - 1) / run : units + extra;  // what the row counts for
-    const int row = (int)(y / runs), r0 = (int)(y - (long long)row * runs);
+    const int row = y / runs, r0 = y - row * runs;
     const int u0 = run ? r0 * run : max(0, r0 - extra);
-    const int u1 = run ? min(units, u0 + run) : (int)min((long long)units, r0 - extra + (end - x));
-    const long long row_begin = base + (long long)row * runs + extra;  // the first unit's place
-    if (u1 <= u0) break;  // the run ends before the row's first unit
+    const int u1 = run ? min(units, u0 + run) : min(units, r0 - extra + (end - x));
+    const int row_begin = base + row * runs + extra;  // the first unit's place
+    if (u1 <= u0) break;  // the share ends before the row's first unit
     const int kvh = row / g.blocks, hb = row - kvh * g.blocks;
     const int heads = min(HB, g.row_heads - hb * HB);   // real query heads of this block
     const int head0 = kvh * g.row_heads + hb * HB;
@@ -423,24 +431,32 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
     // ---- the query's parts, and the factors from a product to an exponent of two -----------------
     // k steps 2 i and 2 i + 1 of part p, block nt lie together: lane l's two fragments in 16 bytes.
     float f1[NT][2], f2;
+    // entries of this lane's head for k step ks
+    auto query = [&](int nt, int ks) {
+      const int h = nt * 8 + r;
+      const int d = S::E4M3 ? 64 * (ks / 4) + 16 * c + 4 * (ks % 4) : 32 * (ks / 2) + 8 * c + 4 * (ks % 2);
+      return h < heads && d < D ? *reinterpret_cast<const float4*>(g.a.q + seq * g.a.q_stride + (head0 + h) * D + d)
+                                : make_float4(0, 0, 0, 0);
+    };
+    constexpr int PAIRS = (S::KS / 2 + W - 1) / W;  // this warp prepares pairs warp, warp + W, ...
+    constexpr int HELD = S::E4M3 ? S::KS : 2 * PAIRS;  // 8-bit caches need a head's largest entry
+    float4 held[NT][HELD];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < HELD; ++k) held[nt][k] = query(nt, S::E4M3 ? k : 2 * (k / 2 * W + warp) + k % 2);
     auto prepare_query = [&] {
       const float cap = g.a.prm.softcap;
       f2 = cap * kLog2e;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int h = nt * 8 + r;
-        const float* q = g.a.q + seq * g.a.q_stride + (long long)(head0 + min(h, heads - 1)) * D;
-        auto entries = [&](int ks) {  // entries of this lane's head for k step ks
-          const int d = S::E4M3 ? 64 * (ks / 4) + 16 * c + 4 * (ks % 4) : 32 * (ks / 2) + 8 * c + 4 * (ks % 2);
-          return h < heads && d < D ? *reinterpret_cast<const float4*>(q + d) : make_float4(0, 0, 0, 0);
-        };
         float up = 1.0f, down = 1.0f;
         if constexpr (S::E4M3) {
           // fp16 parts: the head's largest entry is brought to [2^9, 2^10)
           float top = 0.0f;
 #pragma unroll
           for (int ks = 0; ks < S::KS; ++ks) {
-            const float4 v = entries(ks);
+            const float4 v = held[nt][ks];
             top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
           }
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
@@ -452,11 +468,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
             down = __uint_as_float((uint32_t)(127 - k) << 23);
           }
         }
-#pragma unroll
-        for (int i = 0; i < (S::KS / 2 + W - 1) / W; ++i) {
-          const int pair = i * W + warp;
-          if (pair >= S::KS / 2) break;
-          float4 v = entries(2 * pair), w = entries(2 * pair + 1);
+        auto put = [&](int pair, float4 v, float4 w) {
           v.x *= up, v.y *= up, v.z *= up, v.w *= up;
           w.x *= up, w.y *= up, w.z *= up, w.w *= up;
 #pragma unroll
@@ -467,6 +479,15 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
                              qsm + ((pair * S::QP + p) * NT + nt) * 512 + lane * 16),
                          "r"(x0), "r"(x1), "r"(y0), "r"(y1));
           }
+        };
+        if constexpr (S::E4M3) {
+#pragma unroll
+          for (int pair = 0; pair < S::KS / 2; ++pair)
+            if (pair % W == warp) put(pair, held[nt][2 * pair], held[nt][2 * pair + 1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < PAIRS; ++i)
+            if (i * W + warp < S::KS / 2) put(i * W + warp, held[nt][2 * i], held[nt][2 * i + 1]);
         }
         // the columns of a score fragment are heads 2c, 2c + 1
         const float f = g.a.prm.scale * C.k_scale * down * (cap > 0.0f ? 1.0f / cap : kLog2e);
@@ -844,28 +865,32 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
     const int quads = D / 4;
     for (int e = tid; e < heads * quads; e += T) {
       const int h = e / quads, d = (e - h * quads) * 4;
+      float2 ml[W];
+      float4 t[W], v = make_float4(0, 0, 0, 0);
       float M = -INFINITY, L = 0.0f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) M = fmaxf(M, warp_ml[w][h].x);
-      float4 v = make_float4(0, 0, 0, 0);
+      for (int w = 0; w < W; ++w) {
+        ml[w] = warp_ml[w][h];
+        t[w] = *reinterpret_cast<const float4*>(os + (w * HB + h) * S::OS + d);
+      }
+#pragma unroll
+      for (int w = 0; w < W; ++w) M = fmaxf(M, ml[w].x);  // drops a NaN: its sum is NaN too
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        // fmaxf drops a NaN maximum; its warp's sum is NaN and brings it back
-        const float f = warp_ml[w][h].x == -INFINITY ? 0.0f : exp2_ftz(warp_ml[w][h].x - M);
-        if (f == 0.0f && warp_ml[w][h].y == 0.0f) continue;
-        const float4 t = *reinterpret_cast<const float4*>(os + (w * HB + h) * S::OS + d);
-        L += f * warp_ml[w][h].y;
-        v.x += f * t.x, v.y += f * t.y, v.z += f * t.z, v.w += f * t.w;
+        const float f = ml[w].x == -INFINITY ? 0.0f : exp2_ftz(ml[w].x - M);
+        L += f * ml[w].y;
+        v.x += f * t[w].x, v.y += f * t[w].y, v.z += f * t[w].z, v.w += f * t[w].w;
       }
       put_row<S>(g, whole ? -1 : slot, (long long)seq * g.a.n_heads + head0, h, d, v, M, L);
     }
 
     // ---- a shared row: the last CTA to arrive joins its parts ----------------------------------------
     if (!whole) {
-      const int b0 = run ? (int)row_begin : (int)(((row_begin + 1) * B - 1) / U);
-      const int n = run ? runs : (int)(((row_begin + units) * B - 1) / U) - b0 + 1;
+      auto owner = [&](int unit) { return (int)(((unit + 1ll) * B - 1) / U); };  // start_of's inverse
+      const int b0 = run ? row_begin : owner(row_begin);
+      const int n = run ? runs : owner(row_begin + units - 1) - b0 + 1;
       // the first CTA's slot: its first segment if its run starts in this row
-      const int slot0 = 2 * b0 + (run || row_begin <= U * b0 / B ? 0 : 1);
+      const int slot0 = 2 * b0 + (run || row_begin <= start_of(b0) ? 0 : 1);
       const long long at = (long long)seq * g.a.n_heads + head0;
       auto slot_of = [&](int k) { return k == 0 ? slot0 : 2 * (b0 + k); };
       // In one step up to kJoin parts; else groups of about sqrt(n) first, each by its own last CTA,
@@ -889,9 +914,10 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
     x += runs - r0;
     if (x == base + rows_of_seq * runs) {
       base = x;
-      ++seq;
+      len = len_at(++seq);
     }
   }
+  leftovers();
 }
 
 constexpr int kMaxCtas = 4;  // CTAs on an SM, over all shapes
