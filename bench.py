@@ -895,12 +895,116 @@ def run_scaled_guess(args, dev):
     return out
 
 
+HEADS, HEAD_DIM, KV_PAGE = 32, 128, 16  # the block's attention: one key head for each query head
+LAYER_CONTEXTS = (512, 4096)
+
+
+def run_decode_layer(args, dev):
+    """The whole decoder layer of the headline's block as a decoder runs it, one token at a time:
+    residual norm, qkv, cache append with rotation, attention over the paged cache, o, residual
+    norm, gate/up, down (fed in its own launch), residual sum. Each token reads its own weight
+    replica and cache, so all of it streams from HBM. Beside it, the four projections alone on the
+    same inputs: the difference is what the steps between them add."""
+    from tiered_weight_gemv_b200 import spax, synth
+
+    n_tok, n_rep = 16, 4
+    steps, warmup = max(5, min(args.steps, 20)), args.warmup
+    stream = torch.cuda.Stream(device=dev)
+    mats = make_weights(dev)
+    sites = {}
+    for name, d_out, d_in, _ in SITES:
+        kf, ka = k_counts(d_in)
+        pm = spax.alloc_packed(d_out, d_in, spax.FULL_BF16, device=dev)
+        spax.spax_pack_weights(mats[name], spax.FULL_BF16, pm)
+        reps = [pm] + [spax.PackedMatrix(d_out, d_in, spax.FULL_BF16, pm.full.clone(), pm.approx.clone())
+                       for _ in range(n_rep - 1)]
+        sites[name] = dict(reps=reps, descs=[r.desc() for r in reps],
+                           prm=spax.mask_params(spax.MASK_TOPK, k_full=kf, k_approx=ka),
+                           y=torch.empty(n_tok, d_out, device=dev),
+                           ws=spax.alloc_workspace(spax.OP_TIERED_GEMV, d_out, d_in, device=dev))
+    del mats
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    ones = torch.ones(HIDDEN, dtype=torch.bfloat16, device=dev)
+    norm = spax.Norm(ones)
+    rope = spax.Rope(10000.0 ** (-torch.arange(HEAD_DIM // 2, dtype=torch.float64, device=dev)
+                                 / (HEAD_DIM // 2)))
+    h = synth.laplace((n_tok, 1, HIDDEN), 0, 801, device=dev)
+    x1, r, x2, r2 = (torch.empty_like(h) for _ in range(4))
+    att = torch.empty(n_tok, 1, HEADS, HEAD_DIM, device=dev)
+    out = {"tokens": n_tok, "weight_replicas": n_rep, "heads": HEADS, "head_dim": HEAD_DIM,
+           "cache": "bf16, pages of %d" % KV_PAGE}
+
+    def gemv(name, t, x):
+        s = sites[name]
+        spax.spax_masked_gemv(s["reps"][t % n_rep], x, s["prm"], s["y"][t], st, s["ws"],
+                              desc=s["descs"][t % n_rep])
+
+    def down(t):
+        s = sites["down"]
+        spax.spax_masked_gemv_swiglu(s["reps"][t % n_rep], sites["gate_up"]["y"][t], s["prm"],
+                                     s["y"][t], st, s["ws"], desc=s["descs"][t % n_rep])
+
+    for ctx in LAYER_CONTEXTS:
+        pages = -(-ctx // KV_PAGE)
+        n_cache = max(n_rep, math.ceil(3 * L2_BYTES / (ctx * HIDDEN * 4)))  # 4 B: key and value
+        caches = []
+        for c in range(n_cache):
+            kv = spax.alloc_kv_cache(pages, KV_PAGE, HEADS, HEAD_DIM, device=dev)
+            for pool in (kv.k, kv.v):
+                pool.normal_()
+            caches.append(kv)
+        aws = spax.alloc_attention_workspace(caches[0], HEADS)
+        table = torch.randperm(pages, device=dev).int().view(1, pages)
+        pos = torch.full((1,), ctx - 1, dtype=torch.int32, device=dev)
+        lens = torch.full((1,), ctx, dtype=torch.int32, device=dev)
+
+        def between(t):  # qkv's row -> the attention's output
+            kv = caches[t % n_cache]
+            q, k, v = sites["qkv"]["y"][t].view(1, 3, HEADS, HEAD_DIM).unbind(1)
+            spax.spax_kv_append(kv, q, k, v, pos, table, st, rope=rope)
+            spax.spax_paged_attention(kv, q, table, lens, att[t], st, aws, scale=HEAD_DIM ** -0.5)
+
+        def layer():
+            for t in range(n_tok):
+                spax.spax_residual_norm(h[t], None, None, x1[t], pre=norm)
+                gemv("qkv", t, x1[t].view(-1))
+                between(t)
+                gemv("o", t, att[t].view(-1))
+                spax.spax_residual_norm(h[t], sites["o"]["y"][t].view(1, -1), r[t], x2[t], pre=norm)
+                gemv("gate_up", t, x2[t].view(-1))
+                down(t)
+                spax.spax_residual_norm(r[t], sites["down"]["y"][t].view(1, -1), r2[t], None)
+
+        def projections():
+            for t in range(n_tok):
+                gemv("qkv", t, x1[t].view(-1))
+                gemv("o", t, att[t].view(-1))
+                gemv("gate_up", t, x2[t].view(-1))
+                down(t)
+
+        whole = _timed_graph(layer, stream, steps, warmup) * 1000 / n_tok
+        alone = _timed_graph(projections, stream, steps, warmup) * 1000 / n_tok
+        out[f"context_{ctx}"] = {
+            "layer_us_per_token": round(whole, 3), "projections_us_per_token": round(alone, 3),
+            "between_us_per_token": round(whole - alone, 3),
+            "cache_bytes": ctx * HIDDEN * 4, "caches": n_cache,
+            "cache_us_at_8TBps": round(ctx * HIDDEN * 4 / 8e6, 3)}
+        if int(st.item()) != 0:
+            raise RuntimeError(f"device status {int(st.item())} in the decoder layer")
+        del caches
+        torch.cuda.empty_cache()
+    del sites
+    torch.cuda.empty_cache()
+    return out
+
+
 def run_extras(args, dev):
     """Measurements beside the headline, on one GPU, each a CUDA graph timed like the headline."""
     out = {"dequant_vs_load": run_dequant(args, dev)}
     out["guess_under_token_scale"] = run_scaled_guess(args, dev)
     out["llama3_8b_stack"] = run_llama3_stack(args, dev)
     out["llama2_70b_mlp_int4"] = run_llama2_70b_mlp(args, dev)
+    out["decode_layer"] = run_decode_layer(args, dev)
     out["host_link_offload"] = run_host_link(args, dev)
     torch.cuda.empty_cache()
     return out

@@ -457,7 +457,8 @@ uint64_t spax_weight_bytes(int d_out, int full_fmt, int64_t n_full, int64_t n_ap
  * the GPU). One layer: norm -> masked GEMV (qkv) -> append -> attention -> masked GEMV (o) -> norm
  * -> masked GEMV (gate/up) -> masked GEMV (down, _swiglu). Activations are fp32 throughout, as the
  * GEMVs take and give them; the calls also take batches and prompts (one row for each token).
- * Values are not checked for being finite: a NaN or Inf goes through the formulas.
+ * Values are not checked for being finite: a NaN or Inf goes through the formulas (an infinite query
+ * entry makes its head NaN).
  */
 
 typedef enum { SPAX_KV_BF16 = 0, SPAX_KV_E4M3 = 1 } spax_kv_dtype;
@@ -534,8 +535,8 @@ spax_status spax_kv_append(const spax_kv_cache* h_cache, const float* d_q, int64
 
 /*
  * Scores of spax_paged_attention: s_j = scale * (q . k_j), then softcap * tanh(s_j / softcap) when
- * softcap > 0. window > 0: only the last `window` positions are seen; 0: all. scale finite,
- * softcap >= 0 and finite, window >= 0.
+ * softcap > 0. window > 0: only the last `window` positions are seen; 0: all. scale finite, softcap
+ * 0 or within [2^-60, 2^60], window >= 0.
  */
 typedef struct {
   float scale;

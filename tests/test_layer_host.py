@@ -103,6 +103,8 @@ def test_append_refuses(kw, want):
     (dict(prm=None), spax.ERR_ARG), (dict(prm=(math.nan, 0.0, 0)), spax.ERR_ARG),
     (dict(prm=(math.inf, 0.0, 0)), spax.ERR_ARG), (dict(prm=(1.0, -1.0, 0)), spax.ERR_ARG),
     (dict(prm=(1.0, math.inf, 0)), spax.ERR_ARG), (dict(prm=(1.0, 0.0, -1)), spax.ERR_ARG),
+    (dict(prm=(1.0, 1e-30, 0)), spax.ERR_ARG), (dict(prm=(1.0, 1e30, 0)), spax.ERR_ARG),
+    (dict(n=65535, max_pages=1 << 20, out=1 << 40), spax.ERR_SHAPE), (dict(n=65536), spax.ERR_SHAPE),
     (dict(n=-1), spax.ERR_SHAPE), (dict(H=0), spax.ERR_SHAPE), (dict(H=5), spax.ERR_SHAPE),
     (dict(table=None), spax.ERR_ARG), (dict(lens=None), spax.ERR_ARG), (dict(out=None), spax.ERR_ARG),
     (dict(q=None), spax.ERR_ARG), (dict(q=A + 4), spax.ERR_ARG), (dict(out=4 * A + 8), spax.ERR_ARG),

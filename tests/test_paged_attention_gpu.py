@@ -119,6 +119,20 @@ def test_one_sequence_split_over_its_length(lens, H, K, D, dtype):
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("H,K,D,dtype", [(8, 1, 80, 0), (8, 1, 112, 1), (5, 1, 48, 0), (16, 2, 96, 0),
+                                         (6, 1, 176, 1), (12, 1, 16, 0), (16, 1, 112, 1)])
+def test_heads_that_no_warp_holds_alone_are_joined(H, K, D, dtype):
+    """Rows of many parts, joined in two steps by threads of several warps to a head, often enough
+    that their order differs."""
+    for n in (1100, 4000, 17 * 64):
+        case = Case([n, 5, n - 1], H, K, D, dtype, 32, seed=n)
+        first = case.run()
+        case.check(*first)
+        for _ in range(20):
+            again = case.run()
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 @pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 699, 700, 100000])
 @pytest.mark.parametrize("dtype,softcap", [(0, 0.0), (1, 5.0)])
 def test_windows_and_capped_scores(window, dtype, softcap):

@@ -121,7 +121,8 @@ spax_status spax_paged_attention(const spax_kv_cache* h_cache, const float* q, i
   if (st != SPAX_OK) return st;
   if (!h_params) return SPAX_ERR_ARG;
   a.prm = *h_params;
-  if (!std::isfinite(a.prm.scale) || !std::isfinite(a.prm.softcap) || a.prm.softcap < 0.0f ||
+  const float cap = a.prm.softcap;  // its reciprocal is formed too
+  if (!std::isfinite(a.prm.scale) || !(cap == 0.0f || (cap >= 0x1p-60f && cap <= 0x1p60f)) ||
       a.prm.window < 0)
     return SPAX_ERR_ARG;
   if (n_seq < 0 || n_seq > 65535 || n_heads < 1 || n_heads > 65535) return SPAX_ERR_SHAPE;

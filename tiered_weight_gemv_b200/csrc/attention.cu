@@ -164,7 +164,7 @@ struct AttnArgs {
   int blocks;         // blocks of HB query heads to a key head
   bool page16;        // 16 positions from a multiple of 16 are on one page
   float* part;        // [2 CTAs][HB][DP] outputs of shared rows
-  float2* part_ml;    // [2 CTAs][HB] their maxima and sums
+  float2 *part_ml, *part_ml2;  // [2 CTAs][HB] their maxima and sums, and those of joined groups
   uint32_t *tickets, *tickets2;  // [2 CTAs] each, zero at rest
 };
 
@@ -172,7 +172,7 @@ template <class S>
 struct Attn {
   // Positions [lo, len) of a sequence, by the window.
   static __device__ __forceinline__ int clipped_len(const AttnArgs& g, int seq, bool* bad) {
-    const int len = __ldg(g.a.lens + seq);
+    const int len = g.a.lens[seq];
     *bad = len < 0 || len > g.a.max_pages * g.a.cache.page_size;
     return *bad ? 0 : len;
   }
@@ -202,13 +202,14 @@ __device__ __forceinline__ bool arrive(uint32_t* ticket, int n, bool* is_last) {
   return *is_last;
 }
 
-// One head's entries of a row, joined: written as they are to a slot, or divided to the output.
+// One head's entries of a row, joined: written as they are to a slot (the maximum and sum to ml), or
+// divided to the output.
 template <class S>
-__device__ __forceinline__ void put_row(const AttnArgs& g, int slot, long long at, int h, int d, float4 v,
-                                        float M, float L) {
+__device__ __forceinline__ void put_row(const AttnArgs& g, float2* ml, int slot, long long at, int h, int d,
+                                        float4 v, float M, float L) {
   if (slot >= 0) {
     __stcg(reinterpret_cast<float4*>(g.part + ((long long)slot * S::HB + h) * S::DP + d), v);
-    if (d == 0) __stcg(g.part_ml + slot * S::HB + h, make_float2(M, L));
+    if (d == 0) __stcg(ml + slot * S::HB + h, make_float2(M, L));
   } else {
     const float inv = L == 0.0f ? 0.0f : g.a.cache.v_scale / L;
     if (L == 0.0f) v = make_float4(0, 0, 0, 0);
@@ -219,9 +220,12 @@ __device__ __forceinline__ void put_row(const AttnArgs& g, int slot, long long a
 }
 
 // Joins n parts of a row, the slots of which slot_of gives, in their order: a thread takes the
-// maxima, sums and entries of N parts at a time, all in flight at once.
+// maxima, sums and entries of N parts at a time, all in flight at once. A slot that is joined to may
+// be one of the parts: an entry is read and written by one thread alone, while the maximum and sum,
+// which several threads read, go to another array (the second step's).
 template <class S, int N, class F>
-__device__ __forceinline__ void join(const AttnArgs& g, int heads, int n, F slot_of, int to, long long at) {
+__device__ __forceinline__ void join(const AttnArgs& g, const float2* from_ml, int heads, int n, F slot_of,
+                                     int to, long long at) {
   const int quads = g.a.cache.head_dim / 4;
   for (int e = threadIdx.x; e < heads * quads; e += S::THREADS) {
     const int h = e / quads, d = (e - h * quads) * 4;
@@ -236,7 +240,7 @@ __device__ __forceinline__ void join(const AttnArgs& g, int heads, int n, F slot
         t[i] = make_float4(0, 0, 0, 0);
         if (k + i < n) {
           const long long slot = slot_of(k + i);
-          ml[i] = __ldcg(g.part_ml + slot * S::HB + h);
+          ml[i] = __ldcg(from_ml + slot * S::HB + h);
           t[i] = __ldcg(reinterpret_cast<const float4*>(g.part + (slot * S::HB + h) * S::DP + d));
         }
       }
@@ -254,15 +258,16 @@ __device__ __forceinline__ void join(const AttnArgs& g, int heads, int n, F slot
       }
       M = top;
     }
-    put_row<S>(g, to, at, h, d, v, M, L);
+    put_row<S>(g, g.part_ml2, to, at, h, d, v, M, L);
   }
 }
 template <class S, class F>
-__device__ __forceinline__ void join(const AttnArgs& g, int heads, int n, F slot_of, int to, long long at) {
+__device__ __forceinline__ void join(const AttnArgs& g, const float2* from_ml, int heads, int n, F slot_of,
+                                     int to, long long at) {
   if (n <= 4)
-    join<S, 4>(g, heads, n, slot_of, to, at);
+    join<S, 4>(g, from_ml, heads, n, slot_of, to, at);
   else
-    join<S, 16>(g, heads, n, slot_of, to, at);
+    join<S, 16>(g, from_ml, heads, n, slot_of, to, at);
 }
 
 template <class S>
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
     if (2 * rows <= (int)gridDim.x) {
       run = (U + B - 1) / B;
       // a run may be this much longer than equal runs before their row ends cost less
-      const int most = run + max(6, run / 8);
+      const int most = run + max(6, run / 16);
       const int more = few ? max(1, run / 16) : (most - run) / 2;
       for (;; run += more) {
         const int n = rows_of_seq * total([run](int u) { return (u + run - 1) / run; });
@@ -513,7 +518,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       const int mine_at = lane & (TILE - 1);  // this lane's position in a tile
       auto page_entry = [&](int i) {  // the table's entry for the lane's position of tile i
         int pos = first + i * (W * TILE) + (g.page16 ? mine_at & 16 : mine_at);
-        return i < mine ? __ldg(table + A::page_of(g, min(pos, t1 - 1))) : 0;
+        return i < mine ? table[A::page_of(g, min(pos, t1 - 1))] : 0;
       };
       // Where the rows of tile i are, and which of its positions are seen.
       struct Place {
@@ -881,7 +886,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
         L += f * ml[w].y;
         v.x += f * t[w].x, v.y += f * t[w].y, v.z += f * t[w].z, v.w += f * t[w].w;
       }
-      put_row<S>(g, whole ? -1 : slot, (long long)seq * g.a.n_heads + head0, h, d, v, M, L);
+      put_row<S>(g, g.part_ml, whole ? -1 : slot, (long long)seq * g.a.n_heads + head0, h, d, v, M, L);
     }
 
     // ---- a shared row: the last CTA to arrive joins its parts ----------------------------------------
@@ -901,11 +906,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       const int k0 = (b - b0) / group * group, groups = (n + group - 1) / group;
       bool last = arrive(g.tickets + slot_of(k0), min(group, n - k0), &is_last);
       if (last) {
-        join<S>(g, heads, min(group, n - k0), [&](int i) { return slot_of(k0 + i); },
+        join<S>(g, g.part_ml, heads, min(group, n - k0), [&](int i) { return slot_of(k0 + i); },
                 groups == 1 ? -1 : slot_of(k0), at);
         if (groups > 1) {
           last = arrive(g.tickets2 + slot0, groups, &is_last);
-          if (last) join<S>(g, heads, groups, [&](int i) { return slot_of(i * group); }, -1, at);
+          if (last) join<S>(g, g.part_ml2, heads, groups, [&](int i) { return slot_of(i * group); }, -1, at);
         }
       }
     }
@@ -931,7 +936,7 @@ static int padded_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 1
 size_t attention_ws_bytes(int n_heads, int n_kv_heads, int head_dim, int sm_count) {
   const size_t hb = 8 * head_blocks(n_heads / n_kv_heads, head_dim);
   const size_t slots = 2 * kMaxCtas * (size_t)sm_count;  // two for each CTA
-  return slots * hb * (padded_dim(head_dim) * 4 + 8) + ((slots * 8 + 255) & ~size_t(255));
+  return slots * hb * (padded_dim(head_dim) * 4 + 16) + ((slots * 8 + 255) & ~size_t(255));
 }
 
 template <class S>
@@ -945,6 +950,7 @@ static cudaError_t launch_shape(AttnArgs g, int sm_count, cudaStream_t stream) {
   g.tickets2 = g.tickets + slots;
   g.part = reinterpret_cast<float*>(static_cast<uint8_t*>(g.a.ws) + ((slots * 8 + 255) & ~255ll));
   g.part_ml = reinterpret_cast<float2*>(g.part + slots * S::HB * S::DP);
+  g.part_ml2 = g.part_ml + slots * S::HB;
   long long longest = (long long)g.a.max_pages * g.a.cache.page_size;
   if (g.a.prm.window > 0 && g.a.prm.window + kUnit < longest) longest = g.a.prm.window + kUnit;
   const long long units = (long long)g.a.n_seq * g.a.cache.n_kv_heads * g.blocks *
@@ -969,33 +975,29 @@ cudaError_t launch_paged_attention(const AttnLaunch& a, int sm_count, cudaStream
   g.page16 = d % 16 == 0;
   const int dp = padded_dim(a.cache.head_dim), nt = head_blocks(g.row_heads, a.cache.head_dim);
   const bool e = a.cache.dtype == SPAX_KV_E4M3;
-  // warps, slots and CTAs by what fits 227 KB and 65536 registers an SM
-#ifndef CFG64E
-#define CFG64E 64, true, 1, 2, 4, 5, 3
-#define CFG64B 64, false, 1, 2, 4, 3, 3
-#define CFG128E 128, true, 1, 2, 4, 3, 3
-#define CFG128B 128, false, 1, 1, 4, 3, 3
-#define CFG256E 256, true, 1, 1, 4, 5, 2
-#define CFG256B 256, false, 1, 1, 4, 3, 2
-#define CFG64E2 64, true, 2, 1, 4, 7, 3
-#define CFG64B2 64, false, 2, 1, 4, 5, 3
-#define CFG128E2 128, true, 2, 1, 4, 7, 2
-#define CFG128B2 128, false, 2, 1, 4, 5, 2
-#endif
+  // The shape by head_dim (padded), type and query heads to a key head; tiles, warps, slots and CTAs
+  // are what was fastest of what fits 227 KB and 65536 registers an SM. Measured on B200:
+  // - 128-wide bf16, 131071 positions of 8 key heads: 88.9 us; 16 warps an SM (128 registers a
+  //   thread) 96 to 98, tiles of 32 positions with 8 warps 94.5;
+  // - 128-wide 8-bit, 33 x 4099 positions: 56.5 us; tiles of 16 positions 68, 16 warps 62 to 63;
+  // - 256-wide bf16: 8 warps of 3 slots 37.6 us on 48 windows of 2048, 6 warps 63, tiles of 32
+  //   positions 72; 8-bit, 33 x 4099: tiles of 32 positions 102, of 16 113;
+  // - 16 query heads to a key head, ragged batch of 64 up to 8192: bf16 with 12 warps 153, 8 warps 166
+  //   (one sequence alone prefers 8: 40 to 48); 8-bit tiles of 32 positions 89, of 16 99.
   if (dp == 64 && nt == 1)
-    return e ? launch_shape<AttnShape<CFG64E>>(g, sm_count, stream)
-             : launch_shape<AttnShape<CFG64B>>(g, sm_count, stream);
+    return e ? launch_shape<AttnShape<64, true, 1, 2, 4, 5, 3>>(g, sm_count, stream)
+             : launch_shape<AttnShape<64, false, 1, 2, 4, 3, 3>>(g, sm_count, stream);
   if (dp == 64)
-    return e ? launch_shape<AttnShape<CFG64E2>>(g, sm_count, stream)
-             : launch_shape<AttnShape<CFG64B2>>(g, sm_count, stream);
+    return e ? launch_shape<AttnShape<64, true, 2, 2, 4, 3, 3>>(g, sm_count, stream)
+             : launch_shape<AttnShape<64, false, 2, 2, 4, 3, 3>>(g, sm_count, stream);
   if (dp == 128 && nt == 1)
-    return e ? launch_shape<AttnShape<CFG128E>>(g, sm_count, stream)
-             : launch_shape<AttnShape<CFG128B>>(g, sm_count, stream);
+    return e ? launch_shape<AttnShape<128, true, 1, 2, 4, 3, 3>>(g, sm_count, stream)
+             : launch_shape<AttnShape<128, false, 1, 1, 4, 3, 3>>(g, sm_count, stream);
   if (dp == 128)
-    return e ? launch_shape<AttnShape<CFG128E2>>(g, sm_count, stream)
-             : launch_shape<AttnShape<CFG128B2>>(g, sm_count, stream);
-  return e ? launch_shape<AttnShape<CFG256E>>(g, sm_count, stream)
-           : launch_shape<AttnShape<CFG256B>>(g, sm_count, stream);
+    return e ? launch_shape<AttnShape<128, true, 2, 2, 4, 3, 2>>(g, sm_count, stream)
+             : launch_shape<AttnShape<128, false, 2, 1, 4, 3, 3>>(g, sm_count, stream);
+  return e ? launch_shape<AttnShape<256, true, 1, 2, 4, 3, 2>>(g, sm_count, stream)
+           : launch_shape<AttnShape<256, false, 1, 1, 4, 3, 2>>(g, sm_count, stream);
 }
 
 }  // namespace spax

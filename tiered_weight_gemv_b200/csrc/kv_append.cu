@@ -44,9 +44,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendL
   const int t = blockIdx.x, tid = threadIdx.x;
   const int D = a.cache.head_dim, K = a.cache.n_kv_heads, H = a.n_heads;
   const int rot = a.rope.rot_dim, half = rot / 2;
-  const int pos = __ldg(a.pos + t);
-  const int seq = a.seq ? __ldg(a.seq + t) : t;
-  const double f = tid < half ? __ldg(a.rope.d_inv_freq + tid) : 0.0;
+  const int pos = a.pos[t];
+  const int seq = a.seq ? a.seq[t] : t;
+  const double f = tid < half ? a.rope.d_inv_freq[tid] : 0.0;
 
   const uint32_t per_head = D / 8, items = (uint32_t)(H + 2 * K) * per_head;
   const uint32_t first = (blockIdx.y * N) * kAppendThreads + tid;

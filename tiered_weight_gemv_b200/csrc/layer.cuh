@@ -15,7 +15,7 @@ namespace spax {
 __device__ __forceinline__ long long cache_row(const spax_kv_cache& c, const int32_t* row,
                                                int pos) {
   const int at = pos / c.page_size;
-  const int page = __ldg(row + at);
+  const int page = row[at];
   if (page < 0 || page >= c.n_pages) return -1;
   return page * c.page_stride + (long long)(pos - at * c.page_size) * c.token_stride;
 }
