@@ -299,13 +299,25 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
     bool bad;
     return s < n_seq ? A::clipped_len(g, s, &bad) : 0;
   };
-  const bool few = n_seq <= 32;  // a lane for each sequence, and no barriers
-  const int per = few ? 1 : (n_seq + T - 1) / T, s0 = few ? lane : tid * per;
-  const int own_len = few ? len_at(lane) : 0, own_units = A::units_of(g, own_len);
+  // Up to 128 sequences: every warp for itself, 1 or kOwn to a lane, in registers, without barriers.
+  constexpr int kOwn = 4;
+  const bool few = n_seq <= 32 * kOwn;
+  const int per = n_seq <= 32 ? 1 : few ? kOwn : (n_seq + T - 1) / T, s0 = (few ? lane : tid) * per;
+  int own_len[kOwn], own_units[kOwn];
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    own_len[k] = few && k < per ? len_at(s0 + k) : 0;
+    own_units[k] = A::units_of(g, own_len[k]);
+  }
   auto units_at = [&](int s) { return A::units_of(g, len_at(s)); };
   auto total = [&](auto f) -> int {  // sum of f(units) over the sequences
-    if (few) return (int)__reduce_add_sync(~0u, (unsigned)f(own_units));
     unsigned x = 0;
+    if (few) {
+#pragma unroll
+      for (int k = 0; k < kOwn; ++k)
+        if (k < per) x += f(own_units[k]);
+      return (int)__reduce_add_sync(~0u, x);
+    }
     for (int k = 0; k < per; ++k) x += f(units_at(s0 + k));
     x = __reduce_add_sync(~0u, x);
     __syncthreads();
@@ -373,18 +385,35 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
   auto weight = [&](int u) { return rows_of_seq * (run ? (u + run - 1) / run : u ? u + extra : 0); };
   int seq, base, len = 0;
   {
-    const int own = weight(few ? own_units : units_at(s0));
-    int sum = own;
-    for (int k = 1; k < per; ++k) sum += weight(units_at(s0 + k));
+    int sum = 0;
+    if (few) {
+#pragma unroll
+      for (int k = 0; k < kOwn; ++k)
+        if (k < per) sum += weight(own_units[k]);
+    } else {
+      for (int k = 0; k < per; ++k) sum += weight(units_at(s0 + k));
+    }
     int x = sum;  // inclusive scan
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(~0u, x, o);
       if (lane >= o) x += y;
     }
     if (few) {
-      seq = __popc(__ballot_sync(~0u, x <= begin));
-      base = __shfl_sync(~0u, x - own, seq);
-      len = __shfl_sync(~0u, own_len, seq);
+      const int there = __popc(__ballot_sync(~0u, x <= begin));  // the lane that has it
+      int at = x - sum, k = 0, own = own_len[0];
+#pragma unroll
+      for (int i = 0; i + 1 < kOwn; ++i) {
+        if (per == 1) break;
+        const int w = weight(own_units[i]);
+        if (k == i && begin >= at + w) {
+          at += w;
+          ++k;
+          own = own_len[i + 1];
+        }
+      }
+      seq = __shfl_sync(~0u, s0 + k, there);
+      base = __shfl_sync(~0u, at, there);
+      len = __shfl_sync(~0u, own, there);
     } else {
       __syncthreads();
       if (lane == 31) prefix[warp] = x;
