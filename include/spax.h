@@ -524,7 +524,7 @@ typedef struct {
  * one call must differ; where two agree, that row's contents are unspecified.
  * Requires h_rope (NULL: no rotation) as above; d_q, d_k, d_v, d_q_out 16-byte aligned, strides
  * multiples of 4 and at least the row when n_tok > 1; n_tok >= 0 (0: nothing is done); at most 65536
- * heads of each kind; max_pages * page_size < 2^31. No workspace.
+ * heads of each kind; max_pages * page_size at most 2^30. No workspace.
  */
 spax_status spax_kv_append(const spax_kv_cache* h_cache, const float* d_q, int64_t q_stride,
                            const float* d_k, int64_t k_stride, const float* d_v, int64_t v_stride,
@@ -563,7 +563,7 @@ typedef struct {
  * must not run concurrently. No CTA waits for another.
  * Requires n_heads a multiple of n_kv_heads, q_stride a multiple of 4 and at least n_heads *
  * head_dim when n_seq > 1, d_q and d_out 16-byte aligned and not overlapping, n_seq >= 0 (0: nothing
- * is done, at most 65535), max_pages * page_size < 2^31 and n_seq * n_kv_heads * ceil(n_heads /
+ * is done, at most 65535), max_pages * page_size at most 2^30 and n_seq * n_kv_heads * ceil(n_heads /
  * n_kv_heads / 8) * (max_pages * page_size / 64 + 10) < 2^31.
  */
 spax_status spax_paged_attention(const spax_kv_cache* h_cache, const float* d_q, int64_t q_stride,
@@ -599,8 +599,9 @@ typedef struct {
  * (gate_stride 0) or one row for each token (gate_stride >= d). d_r (NULL: not written) may be d_h or d_y;
  * d_x (NULL: not written, h_pre not used) may be d_y or d_h; h_pre NULL with d_x set: x = r. d_r
  * and d_x must differ, and at least one is given. Rows are contiguous. Statistics are in fp32 over
- * values held on the chip, the mean before the deviations.
- * Requires 1 <= d <= 32768, n_tok >= 0 (0: nothing is done), finite scales.
+ * values held on the chip, the mean before the deviations (a row's sum of squares must not overflow
+ * fp32).
+ * Requires 1 <= d <= 32768, 0 <= n_tok <= 2^28 (0: nothing is done), finite scales.
  */
 spax_status spax_residual_norm(const float* d_h, const float* d_y, int n_tok, int d,
                                const spax_norm* h_post, const float* d_gate, int64_t gate_stride,

@@ -33,9 +33,9 @@ static spax_status check_cache(const spax_kv_cache* h, spax_kv_cache* c) {
   return SPAX_OK;
 }
 
-// A table of max_pages pages for each sequence, whose positions are 32-bit.
+// A table of max_pages pages for each sequence; sums of a position and a tile's stride fit 32 bits.
 static bool pages_ok(const spax_kv_cache& c, int max_pages) {
-  return max_pages >= 1 && (long long)max_pages * c.page_size <= INT_MAX;
+  return max_pages >= 1 && (long long)max_pages * c.page_size <= 1 << 30;
 }
 
 // Rows of `width` floats: aligned for 16-byte accesses, and apart from one another.
@@ -175,7 +175,7 @@ spax_status spax_residual_norm(const float* h, const float* y, int n_tok, int d,
   spax_status st = check_norm(h_post);
   if (st == SPAX_OK) st = check_norm(h_pre);
   if (st != SPAX_OK) return st;
-  if (n_tok < 0 || d < 1 || d > 32768) return SPAX_ERR_SHAPE;
+  if (n_tok < 0 || n_tok > (1 << 28) || d < 1 || d > 32768) return SPAX_ERR_SHAPE;
   if (!std::isfinite(res_scale) || !std::isfinite(out_scale)) return SPAX_ERR_ARG;
   if (n_tok == 0) return SPAX_OK;
   if (!h || (!r && !x) || (!y && (h_post || gate))) return SPAX_ERR_ARG;

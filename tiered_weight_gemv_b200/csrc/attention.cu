@@ -24,9 +24,17 @@
 // lie together in the cache as the fragment's entries and the query is laid out to match; for V the
 // pairs of positions that a fragment wants are woven from two rows by byte permutes.
 //
-// Precision: cache elements are exact in bf16 (8-bit ones in fp16); fp32 queries and probabilities
-// enter as three parts of 8 (11) bits each, which together hold the value, smallest part first. The
-// matrix instructions add with truncation, so sums over many tiles are kept outside of them.
+// Precision: cache elements are exact in bf16 (8-bit ones in fp16). fp32 queries and probabilities
+// enter as parts of 8 bits (three), in fp16 as parts of 11 bits (three of a query; two of a
+// probability, which leave at most 2^-24 of it), smallest first. The matrix instructions add with
+// truncation, so sums over many tiles are kept outside of them. Against 64 bits the outputs are 2e-7
+// to 7e-7 off (2-norm), less than elementary fp32 operations.
+//
+// Measured on B200 (6.55 TB/s is a copy's rate): 131071 positions of 8 key heads 90 us, 5.96 TB/s; a
+// ragged batch of 64 up to 8192 115 us, 6.29 TB/s; 33 x 4099 positions of an 8-bit cache 56 us, 4.99
+// TB/s: there the instructions bound it (24 a position, one and a half issued a cycle) and the start
+// and end of a CTA, about 3.5 and 1.5 us. One token of 32 heads over 517 positions 9.5 us: launch 2,
+// start-up 2 (lengths, dealing, page table), copies and tiles 2, the join 1.5.
 #include <type_traits>
 
 #include "layer.cuh"
@@ -88,13 +96,6 @@ __device__ __forceinline__ float exp2_ftz(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// (x, y) += (a, b), two lanes an instruction.
-__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
-  asm("{ .reg .b64 p, q; mov.b64 p, {%0, %1}; mov.b64 q, {%2, %3}; add.rn.f32x2 p, p, q; mov.b64 {%0, %1}, p; }"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -846,7 +847,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
                     mma16816<S::E4M3, false>(t, a, pb[mt][nt][k][0], pb[mt][nt][k][1]);
                 }
 #pragma unroll
-              for (int k = 0; k < 4; k += 2) add2(o[nt][4 * j + q][k], o[nt][4 * j + q][k + 1], t[k], t[k + 1]);
+              for (int k = 0; k < 4; ++k) o[nt][4 * j + q][k] += t[k];
             }
           }
         }

@@ -474,47 +474,38 @@ def alloc_workspace(op: int, d_out: int, d_in: int, device="cuda") -> torch.Tens
 # ------------------------------------------------------------- the decode layer between projections
 
 # These calls stand between kernels of a few microseconds, so their argument checks are kept short:
-# one look at each tensor's type, device and address, and the stream's handle without its object.
+# each tensor's type, device and layout in place, the wording of an error only where one fails
+# (_refuse), and the stream's handle without its object.
 _f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
 _device = getattr(torch._C, "_cuda_getDevice", None)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _refuse(t, dtype, dev: int, name: str):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+def _refuse(dtype, dev: int, **tensors):
+    """Words the error of the first of these tensors that is not of the type, on the device and (rows
+    with a name in capitals may be strided) contiguous."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name.lower()} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name.lower()} must be {dtype}, got {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name.lower()} is on cuda:{t.get_device()}, the current device is "
+                             f"cuda:{dev}")
+        if name.islower() and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
 
-def _on(t, dtype, dev: int, name: str) -> int:
-    """The address of a tensor of the current device; rows may be strided."""
-    if t.dtype is not dtype or t.get_device() != dev:
-        _refuse(t, dtype, dev, name)
-    return t.data_ptr()
-
-
-def _whole(t, dtype, dev: int, name: str):
-    """The address of a contiguous tensor of the current device (None: a null pointer)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.get_device() != dev:
-        _refuse(t, dtype, dev, name)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _heads(t: torch.Tensor, d: int, name: str):
-    """(tokens, heads, the tokens' stride) of [tokens, heads, d] whose heads are contiguous."""
-    shape = t.shape
-    if len(shape) != 3 or shape[2] != d:
-        raise ValueError(f"{name} must be [tokens, heads, {d}]")
-    stride = t.stride()
-    if stride[2] != 1 or (stride[1] != d and shape[1] > 1 and shape[0] > 0):
+def _row_stride(t: torch.Tensor, n: int, heads: int, d: int, name: str) -> int:
+    """The tokens' stride of [n, heads, d] whose heads are contiguous."""
+    if t.shape != (n, heads, d):
+        raise ValueError(f"{name} must be [{n}, {heads}, {d}], got {list(t.shape)}")
+    row, head, entry = t.stride()
+    if entry != 1 or (head != d and heads > 1 and n > 0):
         raise ValueError(f"{name}'s heads must be contiguous within a token")
-    return shape[0], shape[1], stride[0]
+    return row
 
 
 class KvCache:
@@ -562,11 +553,10 @@ class Rope:
     of each pair; pairs (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved."""
 
     def __init__(self, inv_freq: torch.Tensor, interleaved: bool = False):
-        dev = inv_freq.get_device() if inv_freq.is_cuda else -1
-        ptr = _whole(inv_freq, torch.float64, dev, "inv_freq") if dev >= 0 else _refuse(
-            inv_freq, torch.float64, dev, "inv_freq")
+        dev = inv_freq.get_device()
+        _refuse(torch.float64, dev, inv_freq=inv_freq)
         self.inv_freq, self.interleaved, self._dev = inv_freq, bool(interleaved), dev
-        self._desc = spax_rope(2 * inv_freq.numel(), int(self.interleaved), ptr)
+        self._desc = spax_rope(2 * inv_freq.numel(), int(self.interleaved), inv_freq.data_ptr())
         self._ref = ctypes.byref(self._desc)
 
 
@@ -585,9 +575,8 @@ class Norm:
         self.d = given[0].numel() if given else None
         self.device = given[0].get_device() if given else None
         dt = types.pop()
-        ptrs = [_whole(t, dt, self.device, n) for t, n in ((weight, "weight"), (bias, "bias"))]
-        if self.device == -1:
-            raise TypeError("weight and bias must be CUDA tensors")
+        _refuse(dt, self.device, weight=weight, bias=bias)
+        ptrs = [None if t is None else t.data_ptr() for t in (weight, bias)]
         self._desc = spax_norm(kind, int(dt == torch.bfloat16), *ptrs, eps)
         self._ref = ctypes.byref(self._desc)
 
@@ -598,13 +587,6 @@ class Norm:
         return self._ref
 
 
-def _at_home(obj, dev: int, name: str):
-    """The descriptor of an object whose tensors are on the current device."""
-    if obj._dev != dev:
-        raise ValueError(f"the {name} is on cuda:{obj._dev}, the current device is cuda:{dev}")
-    return obj._ref
-
-
 def spax_kv_append(cache: KvCache, q, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
                    page_table: torch.Tensor, status: torch.Tensor, rope=None, seq=None, q_out=None,
                    stream=None) -> None:
@@ -613,33 +595,47 @@ def spax_kv_append(cache: KvCache, q, k: torch.Tensor, v: torch.Tensor, pos: tor
     keys and values alone. q_out None: q is rotated in place. pos, seq int32 [tokens] (seq None:
     token t is of sequence t), page_table int32 [sequences, pages]; pos < 0 marks padding."""
     dev, d, heads_kv = _device(), cache.head_dim, cache.n_kv_heads
-    n, kh, ks = _heads(k, d, "k")
-    nv, vh, vs = _heads(v, d, "v")
-    nq, heads, qs, os_, qp, op = n, 0, 0, 0, None, None
+    n = pos.numel()
+    ks = _row_stride(k, n, heads_kv, d, "k")
+    vs = _row_stride(v, n, heads_kv, d, "v")
+    heads = qs = os_ = 0
+    qp = op = sq = None
     if q is not None:
-        nq, heads, qs = _heads(q, d, "q")
-        qp = _on(q, _f32, dev, "q")
-        if q_out is None:
-            os_, op = qs, qp
-        else:
-            if q_out.shape != q.shape:
-                raise ValueError("q_out's size does not match q")
-            os_, op = _heads(q_out, d, "q_out")[2], _on(q_out, _f32, dev, "q_out")
+        heads = q.shape[1] if q.dim() == 3 else 0
+        os_ = qs = _row_stride(q, n, heads, d, "q")
+        qp = op = q.data_ptr()
+        if q.dtype is not _f32 or q.get_device() != dev:
+            _refuse(_f32, dev, Q=q)
+        if q_out is not None:
+            os_ = _row_stride(q_out, n, heads, d, "q_out")
+            op = q_out.data_ptr()
+            if q_out.dtype is not _f32 or q_out.get_device() != dev:
+                _refuse(_f32, dev, Q_OUT=q_out)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if (nq != n or nv != n or kh != heads_kv or vh != heads_kv or pos.numel() != n
-            or (seq is not None and seq.numel() != n)):
-        raise ValueError("q / k / v / pos / seq sizes do not match the cache or one another")
+    if (k.dtype is not _f32 or v.dtype is not _f32 or k.get_device() != dev
+            or v.get_device() != dev):
+        _refuse(_f32, dev, K=k, V=v)
+    if (pos.dtype is not _i32 or page_table.dtype is not _i32 or status.dtype is not _i32
+            or pos.get_device() != dev or page_table.get_device() != dev
+            or status.get_device() != dev or not pos.is_contiguous()
+            or not page_table.is_contiguous()):
+        _refuse(_i32, dev, pos=pos, page_table=page_table, status=status)
     n_seq, max_pages = page_table.shape
-    if seq is None and n_seq < n:
+    if seq is not None:
+        sq = seq.data_ptr()
+        if (seq.dtype is not _i32 or seq.get_device() != dev or not seq.is_contiguous()
+                or seq.numel() != n):
+            _refuse(_i32, dev, seq=seq)
+            raise ValueError("seq's size does not match pos")
+    elif n_seq < n:
         raise ValueError("page_table has fewer rows than there are tokens")
+    if cache._dev != dev or (rope is not None and rope._dev != dev):
+        raise ValueError(f"the cache or rope is not on the current device, cuda:{dev}")
     st = _lib.spax_kv_append(
-        _at_home(cache, dev, "cache"), qp, qs, _on(k, _f32, dev, "k"), ks, _on(v, _f32, dev, "v"),
-        vs, n, heads, _whole(seq, _i32, dev, "seq"), _whole(pos, _i32, dev, "pos"),
-        _whole(page_table, _i32, dev, "page_table"), n_seq, max_pages,
-        None if rope is None else _at_home(rope, dev, "rope"), op, os_,
-        _whole(status, _i32, dev, "status"),
-        _raw_stream(dev) if stream is None else stream.cuda_stream)
+        cache._ref, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, n, heads, sq, pos.data_ptr(),
+        page_table.data_ptr(), n_seq, max_pages, None if rope is None else rope._ref, op, os_,
+        status.data_ptr(), _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise SpaxError("spax_kv_append", st)
 
@@ -664,23 +660,33 @@ def spax_paged_attention(cache: KvCache, q: torch.Tensor, page_table: torch.Tens
     """Attention of one new token of each sequence over the cache: q fp32 [sequences, heads,
     head_dim] (the sequences' stride free), seq_lens int32 [sequences] counting the new token, out
     fp32 as q, contiguous; lse (optional) fp32 [sequences, heads]."""
-    dev = _device()
-    n, heads, qs = _heads(q, cache.head_dim, "q")
-    if out.shape != q.shape or seq_lens.numel() != n:
-        raise ValueError("q / out / seq_lens sizes do not match one another")
-    if lse is not None and lse.numel() != n * heads:
-        raise ValueError("lse must be [sequences, heads]")
+    dev, d = _device(), cache.head_dim
+    n = seq_lens.numel()
+    heads = q.shape[1] if q.dim() == 3 else 0
+    qs = _row_stride(q, n, heads, d, "q")
     n_seq, max_pages = page_table.shape
-    if n_seq < n:
-        raise ValueError("page_table has fewer rows than there are sequences")
+    if out.shape != q.shape or n_seq < n or (lse is not None and lse.numel() != n * heads):
+        raise ValueError("out / page_table / lse sizes do not match q and seq_lens")
+    if (q.dtype is not _f32 or out.dtype is not _f32 or q.get_device() != dev
+            or out.get_device() != dev or not out.is_contiguous()):
+        _refuse(_f32, dev, Q=q, out=out)
+    if lse is not None and (lse.dtype is not _f32 or lse.get_device() != dev
+                            or not lse.is_contiguous()):
+        _refuse(_f32, dev, lse=lse)
+    if (page_table.dtype is not _i32 or seq_lens.dtype is not _i32 or status.dtype is not _i32
+            or page_table.get_device() != dev or seq_lens.get_device() != dev
+            or status.get_device() != dev or not page_table.is_contiguous()
+            or not seq_lens.is_contiguous()):
+        _refuse(_i32, dev, page_table=page_table, seq_lens=seq_lens, status=status)
+    if ws.dtype is not _u8 or ws.get_device() != dev or not ws.is_contiguous():
+        _refuse(_u8, dev, ws=ws)
+    if cache._dev != dev:
+        raise ValueError(f"the cache is not on the current device, cuda:{dev}")
     st = _lib.spax_paged_attention(
-        _at_home(cache, dev, "cache"), _on(q, _f32, dev, "q"), qs, n, heads,
-        _whole(page_table, _i32, dev, "page_table"), max_pages,
-        _whole(seq_lens, _i32, dev, "seq_lens"),
-        ctypes.byref(spax_attn_params(scale, softcap, window)), _whole(out, _f32, dev, "out"),
-        _whole(lse, _f32, dev, "lse"), _whole(status, _i32, dev, "status"),
-        _whole(ws, _u8, dev, "ws"), ws.numel(),
-        _raw_stream(dev) if stream is None else stream.cuda_stream)
+        cache._ref, q.data_ptr(), qs, n, heads, page_table.data_ptr(), max_pages,
+        seq_lens.data_ptr(), ctypes.byref(spax_attn_params(scale, softcap, window)),
+        out.data_ptr(), None if lse is None else lse.data_ptr(), status.data_ptr(), ws.data_ptr(),
+        ws.numel(), _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise SpaxError("spax_paged_attention", st)
 
@@ -696,19 +702,38 @@ def spax_residual_norm(h: torch.Tensor, y, r, x, pre=None, post=None, gate=None,
     if d == 0:
         raise ValueError("rows must have entries")
     n = h.numel() // d
-    if ((y is not None and y.shape != shape) or (r is not None and r.shape != shape)
-            or (x is not None and x.shape != shape)):
-        raise ValueError("h / y / r / x sizes do not match")
+    yp = rp = xp = gp = None
     gs = 0
+    if h.dtype is not _f32 or h.get_device() != dev or not h.is_contiguous():
+        _refuse(_f32, dev, h=h)
+    if y is not None:
+        yp = y.data_ptr()
+        if (y.dtype is not _f32 or y.get_device() != dev or not y.is_contiguous()
+                or y.shape != shape):
+            _refuse(_f32, dev, y=y)
+            raise ValueError("y's size does not match h")
+    if r is not None:
+        rp = r.data_ptr()
+        if (r.dtype is not _f32 or r.get_device() != dev or not r.is_contiguous()
+                or r.shape != shape):
+            _refuse(_f32, dev, r=r)
+            raise ValueError("r's size does not match h")
+    if x is not None:
+        xp = x.data_ptr()
+        if (x.dtype is not _f32 or x.get_device() != dev or not x.is_contiguous()
+                or x.shape != shape):
+            _refuse(_f32, dev, x=x)
+            raise ValueError("x's size does not match h")
     if gate is not None:
-        if gate.shape[-1] != d or gate.numel() not in (d, n * d):
+        gp = gate.data_ptr()
+        if gate.dtype is not _f32 or gate.get_device() != dev or not gate.is_contiguous():
+            _refuse(_f32, dev, gate=gate)
+        if gate.dim() == 0 or gate.shape[-1] != d or gate.numel() not in (d, n * d):
             raise ValueError("gate must be [d] or of h's size")
         gs = d if gate.numel() == n * d and gate.dim() > 1 else 0
     st = _lib.spax_residual_norm(
-        _whole(h, _f32, dev, "h"), _whole(y, _f32, dev, "y"), n, d,
-        None if post is None else post._for(d, dev), _whole(gate, _f32, dev, "gate"), gs,
-        res_scale, out_scale, None if pre is None else pre._for(d, dev),
-        _whole(r, _f32, dev, "r"), _whole(x, _f32, dev, "x"),
+        h.data_ptr(), yp, n, d, None if post is None else post._for(d, dev), gp, gs, res_scale,
+        out_scale, None if pre is None else pre._for(d, dev), rp, xp,
         _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise SpaxError("spax_residual_norm", st)
