@@ -1,10 +1,15 @@
 // residual_norm.cu — r = res_scale * h + out_scale * gate * N_post(y), x = N_pre(r), by rows.
 //
-// One CTA for each row, which stays in registers from its load to its last store: h and y are read
-// once, r and x written once, so many rows are bound by HBM and one row by the latency of its loads
-// and of one block sum for each norm (two with a mean: the deviations are taken from the rounded
-// mean itself, in a second sum, not from a difference of squares). Few rows get as many threads as
-// the row has 16-byte pieces; many rows get four pieces a thread, so that several rows share an SM.
+// One CTA for each row (a cluster for a wide one), which stays in registers from its load to its last
+// store: h and y are read once, r and x written once, so many rows are bound by HBM and one row by
+// the latency of its loads and of one block sum for each norm (two with a mean: the deviations are
+// taken from the rounded mean itself, in a second sum, not from a difference of squares).
+//
+// Measured on B200 (a copy's rate is 6.55 TB/s): 8192 rows of 4096, RMS, 81 us (6.63 TB/s); 4001 rows
+// of 5004 with both LAYER norms, biases and a gate of each token 71 us (5.65 TB/s), and of 5003, whose
+// rows start off the 16-byte boundary, 88 us (4.55 TB/s; 132 with single values: the instructions of
+// addresses and checks bound it). One row of 4096 2.3 us, of 28672 3.2 us (a cluster of 8; 16 us in one
+// CTA, whose registers it overflows).
 #include "layer.cuh"
 
 namespace spax {
@@ -29,17 +34,16 @@ struct Row {
     return full || (unsigned)(at + i * 32 * W + k) < (unsigned)d;
   }
 
-  template <bool CHECK, bool ONCE>
+  template <bool CHECK>
   __device__ __forceinline__ void load_as(const float* p, float (&v)[N][W]) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (!CHECK || whole(i)) {
         if constexpr (W == 4) {
-          const float4* q = reinterpret_cast<const float4*>(p + i * 128);
-          const float4 t = ONCE ? __ldcs(q) : *q;
+          const float4 t = *reinterpret_cast<const float4*>(p + i * 128);
           v[i][0] = t.x, v[i][1] = t.y, v[i][2] = t.z, v[i][3] = t.w;
         } else {
-          v[i][0] = ONCE ? __ldcs(p + i * 32) : p[i * 32];
+          v[i][0] = p[i * 32];
         }
       } else if constexpr (SHIFT) {
 #pragma unroll
@@ -48,14 +52,12 @@ struct Row {
       }
     }
   }
-  // The row's values from p (the row's first) on; those outside the row are left as they are. ONCE:
-  // what is read once leaves the caches first.
-  template <bool ONCE>
+  // The row's values from p (the row's first) on; those outside the row are left as they are.
   __device__ __forceinline__ void load(const float* p, float (&v)[N][W]) const {
     if (full)
-      load_as<false, ONCE>(p + at, v);
+      load_as<false>(p + at, v);
     else
-      load_as<true, ONCE>(p + at, v);
+      load_as<true>(p + at, v);
   }
   __device__ __forceinline__ void store(float* p, const float (&v)[N][W]) const {
     p += at;
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(W * N > 8 ? 512 : 1024, W * N > 8 ? 2 : 1)
     if (a.gate_stride == 0)
       R.load_shared(a.gate, v);
     else
-      R.template load<true>(a.gate + token * a.gate_stride, v);
+      R.load(a.gate + token * a.gate_stride, v);
   };
 
   float z[N][W], h[N][W];
@@ -194,8 +196,8 @@ __global__ void __launch_bounds__(W * N > 8 ? 512 : 1024, W * N > 8 ? 2 : 1)
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int k = 0; k < W; ++k) z[i][k] = h[i][k] = 0.0f;
-  if (add) R.template load<true>(a.y + row, z);
-  R.template load<true>(a.h + row, h);
+  if (add) R.load(a.y + row, z);
+  R.load(a.h + row, h);
   if constexpr (kAhead) {
     if (a.gate) load_gate(g);
     if (post) {
@@ -319,26 +321,27 @@ static cudaError_t launch_row(const NormLaunch& a, int ctas, int threads, cudaSt
   return cudaLaunchKernelEx(&cfg, residual_norm_kernel<W, N, SHIFT, AHEAD, true>, a);
 }
 
-// The shape for pieces of W values: few rows get FEW threads at a piece (4 single values) each in a
-// CTA, many rows N pieces a thread; a row of more than a CTA takes a cluster of 2, 4 or 8.
+// The shape for pieces of W values: few rows get as many threads as there are pieces of 4 values (or
+// of four single values), many rows 4 pieces (8 single values) a thread; a row of more than a CTA
+// takes a cluster of 2, 4 or 8 CTAs, which in every shape hold 32768 values.
 template <int W, bool SHIFT, bool AHEAD>
 static cudaError_t launch_width(const NormLaunch& a, cudaStream_t stream) {
+  constexpr int MOST = AHEAD ? (W == 4 ? 1 : 4) : (W == 4 ? 4 : 8);  // pieces a thread
   const int pieces = (a.d + (SHIFT ? 3 : 0) + W - 1) / W;
-  int n = AHEAD ? (W == 4 ? 1 : 4) : (W == 4 ? 4 : 8);
   const int most = AHEAD ? 1024 : 512;  // threads in a CTA
+  int n = MOST;
   while (n > 1 && pieces <= 32 * (n / 2)) n /= 2;
   int ctas = 1;
   while ((long long)ctas * most * n < pieces) ctas *= 2;
-  if (ctas > 8) return cudaErrorInvalidValue;  // not reached: 8 CTAs take 32768 values in every shape
+  if (ctas > 8) return cudaErrorInvalidValue;
   const int threads = ((pieces + ctas * n - 1) / (ctas * n) + 31) / 32 * 32;
-  switch (n) {
-    case 1: return launch_row<W, 1, SHIFT, AHEAD>(a, ctas, threads, stream);
-    case 2: return launch_row<W, 2, SHIFT, AHEAD>(a, ctas, threads, stream);
-    case 4: return launch_row<W, 4, SHIFT, AHEAD>(a, ctas, threads, stream);
-    default: break;
-  }
-  if constexpr (W == 1) return launch_row<1, 8, SHIFT, AHEAD>(a, ctas, threads, stream);
-  return cudaErrorInvalidValue;  // not reached
+  if constexpr (MOST >= 8)
+    if (n == 8) return launch_row<W, 8, SHIFT, AHEAD>(a, ctas, threads, stream);
+  if constexpr (MOST >= 4)
+    if (n == 4) return launch_row<W, 4, SHIFT, AHEAD>(a, ctas, threads, stream);
+  if constexpr (MOST >= 2)
+    if (n == 2) return launch_row<W, 2, SHIFT, AHEAD>(a, ctas, threads, stream);
+  return launch_row<W, 1, SHIFT, AHEAD>(a, ctas, threads, stream);
 }
 
 cudaError_t launch_residual_norm(const NormLaunch& a, int sm_count, cudaStream_t stream) {
