@@ -514,8 +514,8 @@ typedef struct {
  * k_stride and value heads at d_v + t * v_stride (fp32, heads contiguous; strides in floats), so the
  * three may be parts of one qkv row. It is at position d_pos[t] of sequence d_seq[t]; with d_seq NULL
  * it is of sequence t (then n_tok <= n_seq). d_page_table: int32 [n_seq][max_pages].
- *   q: written rotated, fp32, to d_q_out + t * q_out_stride (d_q_out may equal d_q with the same
- *      stride: in place). d_q NULL: no query heads (n_heads 0, d_q_out not used).
+ *   q: written rotated, fp32, to d_q_out + t * q_out_stride: d_q itself with the same stride (in
+ *      place), or memory apart from q, k and v. d_q NULL: no query heads (n_heads 0, d_q_out not used).
  *   k: rotated in fp32, then rounded once to the cache's type; v: rounded. E4M3 stores
  *      round(value / scale), |value / scale| above 448 (infinities too) as 448 with its sign.
  * d_pos[t] < 0 marks padding: nothing of the token is written (cache and q row stay as they were).
@@ -556,7 +556,8 @@ typedef struct {
  * L outside [0, max_pages * page_size] is taken as 0, a page outside [0, n_pages) as not seen, and
  * either sets *d_status = SPAX_ERR_INDEX.
  * Products and sums are in fp32 (queries and probabilities enter the matrix instructions in parts
- * that together hold their fp32 value); the split over the length depends on the lengths and the
+ * that together hold their fp32 value; the sums of e^(s - m) v_j, m up to 8 ln 2 below the largest
+ * s_j, must not overflow); the split over the length depends on the lengths and the
  * GPU model alone, and its parts are joined in a fixed order: the same bits on every run.
  * Workspace: spax_attention_workspace_bytes() bytes, ZEROED BEFORE FIRST USE; every completed call
  * leaves its counters at zero (zero it again after a device error). Calls that share a workspace

@@ -155,6 +155,34 @@ def test_many_sequences():
     assert case.status.item() == 0
 
 
+@pytest.mark.parametrize("n", [31, 32, 33, 127, 128, 129])
+@pytest.mark.parametrize("dtype,window", [(0, 0), (1, 90)])
+def test_numbers_of_sequences(n, dtype, window):
+    """Around the numbers at which the dealing of work changes its form, with empty and long rows."""
+    lens = [(i * 37) % 211 if i % 5 else 0 for i in range(n)]
+    lens[n // 2], lens[-1] = 1500, 0
+    case = Case(lens, 8, 2, 64, dtype, 16, seed=n)
+    out, lse = case.run(window)
+    assert case.status.item() == 0
+    case.check(out, lse, window)
+
+
+@pytest.mark.parametrize("H,K,D", [(128, 1, 64), (96, 2, 128), (71, 1, 64), (40, 1, 256)])
+def test_many_query_heads_to_a_key_head(H, K, D):
+    for dtype in (0, 1):
+        case = Case([700, 0, 33], H, K, D, dtype, 16, seed=H)
+        out, lse = case.run()
+        case.check(out, lse)
+
+
+def test_keys_and_values_of_one_tensor():
+    both = torch.randn(6, 2, 16, 2, 64, device="cuda").to(torch.bfloat16)
+    case = Case([70, 20], 4, 2, 64)
+    case.table = torch.tensor([[5, 0, 2, 3, 1], [4, 1, 0, 0, 0]], dtype=torch.int32, device="cuda")
+    case.c = spax.KvCache(both[:, 0], both[:, 1])
+    case.check(*case.run())
+
+
 def test_large_scores_and_one_hot_rows():
     """Scores of some hundreds: the running maximum moves far, most probabilities vanish."""
     for dtype in (0, 1):
