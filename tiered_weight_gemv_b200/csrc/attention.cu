@@ -194,10 +194,11 @@ struct Attn {
 __device__ __forceinline__ bool arrive(uint32_t* ticket, int n, bool* is_last) {
   __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
-    *is_last = atomicAdd(ticket, 1u) == (uint32_t)(n - 1);
+    // releases what the barrier has gathered of this CTA, acquires what the others released
+    uint32_t before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(ticket) : "memory");
+    *is_last = before == (uint32_t)(n - 1);
     if (*is_last) *ticket = 0;
-    __threadfence();
   }
   __syncthreads();
   return *is_last;
@@ -307,12 +308,13 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
   int own_len[kOwn], own_units[kOwn];
 #pragma unroll
   for (int k = 0; k < kOwn; ++k) {
-    own_len[k] = few && k < per ? len_at(s0 + k) : 0;
+    own_len[k] = few && k < per ? len_at(n_seq == 1 ? 0 : s0 + k) : 0;
     own_units[k] = A::units_of(g, own_len[k]);
   }
   auto units_at = [&](int s) { return A::units_of(g, len_at(s)); };
   auto total = [&](auto f) -> int {  // sum of f(units) over the sequences
     unsigned x = 0;
+    if (n_seq == 1) return f(own_units[0]);  // every lane has it
     if (few) {
 #pragma unroll
       for (int k = 0; k < kOwn; ++k)
@@ -335,12 +337,12 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
   if (U > 0) {
     const int rows = rows_of_seq * total([](int u) { return u > 0; });
     if (2 * rows <= (int)gridDim.x) {
-      run = (U + B - 1) / B;
+      run = U == B ? 1 : (U + B - 1) / B;
       // a run may be this much longer than equal runs before their row ends cost less
       const int most = run + max(6, run / 16);
       const int more = few ? max(1, run / 16) : (most - run) / 2;
       for (;; run += more) {
-        const int n = rows_of_seq * total([run](int u) { return (u + run - 1) / run; });
+        const int n = rows_of_seq * total([run](int u) { return run == 1 ? u : (u + run - 1) / run; });
         if (n <= (int)gridDim.x) {
           B = n;
           break;
@@ -384,8 +386,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
   auto start_of = [&](int k) { return run ? k : U / B * k + U % B * k / B; };
   const int begin = start_of(b), end = start_of(b + 1);
   auto weight = [&](int u) { return rows_of_seq * (run ? (u + run - 1) / run : u ? u + extra : 0); };
-  int seq, base, len = 0;
-  {
+  int seq = 0, base = 0, len = own_len[0];
+  if (n_seq > 1) {
     int sum = 0;
     if (few) {
 #pragma unroll
@@ -447,13 +449,13 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       continue;
     }
     const int y = x - base;
-    const int runs = run ? (units + run - 1) / run : units + extra;  // what the row counts for
-    const int row = y / runs, r0 = y - row * runs;
+    const int runs = run == 1 ? units : run ? (units + run - 1) / run : units + extra;  // what the row counts for
+    const int row = runs == 1 ? y : y / runs, r0 = y - row * runs;
     const int u0 = run ? r0 * run : max(0, r0 - extra);
     const int u1 = run ? min(units, u0 + run) : min(units, r0 - extra + (end - x));
     const int row_begin = base + row * runs + extra;  // the first unit's place
     if (u1 <= u0) break;  // the share ends before the row's first unit
-    const int kvh = row / g.blocks, hb = row - kvh * g.blocks;
+    const int kvh = g.blocks == 1 ? row : row / g.blocks, hb = row - kvh * g.blocks;
     const int heads = min(HB, g.row_heads - hb * HB);   // real query heads of this block
     const int head0 = kvh * g.row_heads + hb * HB;
     const int lo = A::first_seen(g, len);  // positions [t0, t1), of which those from lo are seen
