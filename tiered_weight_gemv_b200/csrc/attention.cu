@@ -30,11 +30,11 @@
 // truncation, so sums over many tiles are kept outside of them. Against 64 bits the outputs are 2e-7
 // to 7e-7 off (2-norm), less than elementary fp32 operations.
 //
-// Measured on B200 (6.55 TB/s is a copy's rate): 131071 positions of 8 key heads 90 us, 5.96 TB/s; a
+// Measured on B200 (6.55 TB/s is a copy's rate): 131071 positions of 8 key heads 87 us, 6.17 TB/s; a
 // ragged batch of 64 up to 8192 115 us, 6.29 TB/s; 33 x 4099 positions of an 8-bit cache 56 us, 4.99
 // TB/s: there the instructions bound it (24 a position, one and a half issued a cycle) and the start
-// and end of a CTA, about 3.5 and 1.5 us. One token of 32 heads over 517 positions 9.5 us: launch 2,
-// start-up 2 (lengths, dealing, page table), copies and tiles 2, the join 1.5.
+// and end of a CTA, about 3 and 1 us. One token of 32 heads over 517 positions 8.6 us: launch 2,
+// start-up 2 (lengths, dealing, page table), copies and tiles 2, the join of nine parts 1.
 #include <type_traits>
 
 #include "layer.cuh"
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       for (int w = 0; w < warp; ++w) x += prefix[w];
       if (x - sum <= begin && begin < x) {
         int at = x - sum, s = s0;
-        for (;; ++s) {
+        for (; s + 1 < n_seq; ++s) {
           const int n = weight(units_at(s));
           if (begin < at + n) break;
           at += n;
@@ -445,16 +445,19 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
   for (int x = begin; x < end;) {
     const int units = A::units_of(g, len);
     if (units == 0) {  // an empty sequence between two others
-      len = len_at(++seq);
+      if (++seq >= n_seq) break;  // (only if lengths change under the call)
+      len = len_at(seq);
       continue;
     }
     const int y = x - base;
-    const int runs = run == 1 ? units : run ? (units + run - 1) / run : units + extra;  // what the row counts for
+    // what the row counts for
+    const int runs = run == 1 ? units : run ? (units + run - 1) / run : units + extra;
     const int row = runs == 1 ? y : y / runs, r0 = y - row * runs;
     const int u0 = run ? r0 * run : max(0, r0 - extra);
     const int u1 = run ? min(units, u0 + run) : min(units, r0 - extra + (end - x));
     const int row_begin = base + row * runs + extra;  // the first unit's place
-    if (u1 <= u0) break;  // the share ends before the row's first unit
+    // the share ends before the row's first unit (or lengths change under the call)
+    if (u1 <= u0 || row >= rows_of_seq) break;
     const int kvh = g.blocks == 1 ? row : row / g.blocks, hb = row - kvh * g.blocks;
     const int heads = min(HB, g.row_heads - hb * HB);   // real query heads of this block
     const int head0 = kvh * g.row_heads + hb * HB;
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       __syncthreads();
     };
 
-    // ---- this warp's tiles: tile i starts at t0 + (i * W + warp) * 16 ------------------------------
+    // ---- this warp's tiles: tile i starts at t0 + (i * W + warp) * TILE ---------------------------
     // Exponents are taken from a base that trails the maximum by up to kSlack powers of two (it moves
     // only when a score passes it by more), and fp16 probabilities are lifted by 2^12 so that their
     // parts stay normal numbers (and their sums are lowered again, exactly, at the end).
