@@ -68,7 +68,7 @@ struct AttnShape {
   static constexpr int SMEM = RING + KS / 2 * QP * NT * 512;  // and the query's parts
   static constexpr int OS = DP + 4;               // row stride of the warps' outputs at the join
   static_assert(WARPS * HB * OS * 4 <= RING, "the join's buffer overlays the ring");
-  static_assert(CTAS * (SMEM + 3072) <= 228 * 1024, "shared memory of the resident CTAs");
+  static_assert(CTAS * (SMEM + 3 * 1024) <= 228 * 1024, "shared memory of the resident CTAs");
 };
 
 // d = a b + c on the matrix unit; ZERO: d = a b.
