@@ -30,10 +30,10 @@
 // truncation, so sums over many tiles are kept outside of them. Against 64 bits the outputs are 2e-7
 // to 7e-7 off (2-norm), less than elementary fp32 operations.
 //
-// Measured on B200 (6.55 TB/s is a copy's rate): 131071 positions of 8 key heads 87 us, 6.17 TB/s; a
-// ragged batch of 64 up to 8192 115 us, 6.29 TB/s; 33 x 4099 positions of an 8-bit cache 56 us, 4.99
+// Measured on B200 (6.55 TB/s is a copy's rate): 131071 positions of 8 key heads 87 to 92 us, 5.8 to 6.2 TB/s; a
+// ragged batch of 64 up to 8192 114 to 118 us, 6.1 to 6.3 TB/s; 33 x 4099 positions of an 8-bit cache 56 us, 4.99
 // TB/s: there the instructions bound it (24 a position, one and a half issued a cycle) and the start
-// and end of a CTA, about 3 and 1 us. One token of 32 heads over 517 positions 8.6 us: launch 2,
+// and end of a CTA, about 3 and 1 us. One token of 32 heads over 517 positions 8.4 us: launch 2,
 // start-up 2 (lengths, dealing, page table), copies and tiles 2, the join of nine parts 1.
 #include <type_traits>
 
