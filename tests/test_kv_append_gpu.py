@@ -199,6 +199,20 @@ def test_far_positions_keep_their_angle():
     assert np.all(np.abs(out.double().cpu().numpy() - want) <= b)
 
 
+def test_more_tokens_than_a_grid_dimension_of_65535():
+    n, per = 70001, 64
+    n_seq = -(-n // per)
+    c, table, qkv, q, k, v = setup(n, 2, 1, 16, 0, 16, False, n_seq, 4)
+    i = torch.arange(n, device="cuda")
+    seq, pos = (i // per).int(), (i % per).int()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.zeros(n, 2, 16, device="cuda")
+    spax.spax_kv_append(c, q, k, v, pos, table, st, seq=seq, q_out=out)
+    at = table[seq.long(), pos.long() // 16].long(), pos.long() % 16
+    assert st.item() == 0 and torch.equal(out, q)
+    assert torch.equal(c.k[at], k.to(torch.bfloat16)) and torch.equal(c.v[at], v.to(torch.bfloat16))
+
+
 def test_another_stream_and_a_captured_call():
     c, table, qkv, q, k, v = setup(5, 8, 2, 128, 0, 16, False, 5, 3)
     rope = spax.Rope(torch.rand(64, dtype=torch.float64, device="cuda"))

@@ -320,6 +320,22 @@ def test_another_stream():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_two_calls_at_once():
+    """Two streams, a workspace each, neither waiting for the other."""
+    cases = [Case([5000, 1, 0, 900], 8, 2, 128, i, 16, seed=i) for i in (0, 1)]
+    want = [c.run() for c in cases]
+    got = [tuple(torch.zeros_like(t) for t in w) for w in want]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(30):
+        for c, s, (out, lse) in zip(cases, streams, got):
+            spax.spax_paged_attention(c.c, c.q, c.table, c.lens, out, c.status, c.ws,
+                                      scale=c.scale, lse=lse, stream=s)
+    torch.cuda.synchronize()
+    for (a, b), (o, l) in zip(want, got):
+        assert torch.equal(a, o) and torch.equal(b, l)
+
+
 def test_offsets_past_32_bits():
     """Keys and values in one allocation whose pages lie 2^30 elements apart."""
     big = torch.zeros((1 << 31) + (1 << 14), dtype=torch.bfloat16, device="cuda")
