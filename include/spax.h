@@ -523,7 +523,7 @@ typedef struct {
  * [0, n_pages) does the same and sets *d_status = SPAX_ERR_INDEX. The tokens' (page, row) places in
  * one call must differ; where two agree, that row's contents are unspecified.
  * Requires h_rope (NULL: no rotation) as above; d_q, d_k, d_v, d_q_out 16-byte aligned, strides
- * multiples of 4 and at least the row when n_tok > 1; n_tok >= 0 (0: nothing is done); at most 65536
+ * multiples of 4, at least the row and at most 2^32 when n_tok > 1; n_tok >= 0 (0: nothing is done); at most 65536
  * heads of each kind; max_pages * page_size at most 2^30. No workspace.
  */
 spax_status spax_kv_append(const spax_kv_cache* h_cache, const float* d_q, int64_t q_stride,
@@ -562,8 +562,8 @@ typedef struct {
  * Workspace: spax_attention_workspace_bytes() bytes, ZEROED BEFORE FIRST USE; every completed call
  * leaves its counters at zero (zero it again after a device error). Calls that share a workspace
  * must not run concurrently. No CTA waits for another.
- * Requires n_heads a multiple of n_kv_heads, q_stride a multiple of 4 and at least n_heads *
- * head_dim when n_seq > 1, d_q and d_out 16-byte aligned and not overlapping, n_seq >= 0 (0: nothing
+ * Requires n_heads a multiple of n_kv_heads, q_stride a multiple of 4, at least n_heads * head_dim
+ * and at most 2^32 when n_seq > 1, d_q and d_out 16-byte aligned and not overlapping, n_seq >= 0 (0: nothing
  * is done, at most 65535), max_pages * page_size at most 2^30 and n_seq * n_kv_heads * ceil(n_heads /
  * n_kv_heads / 8) * (max_pages * page_size / 64 + 10) < 2^31.
  */
@@ -597,7 +597,7 @@ typedef struct {
  *   r = res_scale * h + out_scale * gate * N_post(y),   x = N_pre(r).
  * h: the residual stream; y: the block's output (NULL: the sum is res_scale * h alone, for a
  * model's first norm); h_post NULL: y as it is; d_gate NULL: 1, else fp32 [d] shared by all rows
- * (gate_stride 0) or one row for each token (gate_stride >= d). d_r (NULL: not written) may be d_h or d_y;
+ * (gate_stride 0) or one row for each token (d <= gate_stride <= 2^32). d_r (NULL: not written) may be d_h or d_y;
  * d_x (NULL: not written, h_pre not used) may be d_y or d_h; h_pre NULL with d_x set: x = r. d_r
  * and d_x must differ, and at least one is given. Rows are contiguous. Statistics are in fp32 over
  * values held on the chip, the mean before the deviations (a row's sum of squares must not overflow

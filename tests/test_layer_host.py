@@ -91,6 +91,7 @@ def test_a_null_cache_is_refused():
     (dict(q=A + 4), spax.ERR_ARG), (dict(k=A + 8), spax.ERR_ARG), (dict(v=A + 12), spax.ERR_ARG),
     (dict(q_out=A + 4), spax.ERR_ARG), (dict(qs=252), spax.ERR_ARG), (dict(ks=130), spax.ERR_ARG),
     (dict(vs=0), spax.ERR_ARG), (dict(qos=258), spax.ERR_ARG), (dict(qos=512), spax.ERR_ARG),
+    (dict(ks=(1 << 32) + 4), spax.ERR_ARG), (dict(vs=-128), spax.ERR_ARG),
     (dict(rope=(60, 0, A)), spax.ERR_SHAPE), (dict(rope=(72, 0, A)), spax.ERR_SHAPE),
     (dict(rope=(-8, 0, A)), spax.ERR_SHAPE), (dict(rope=(64, 2, A)), spax.ERR_ARG),
     (dict(rope=(64, 0, None)), spax.ERR_ARG), (dict(rope=(64, 0, A + 4)), spax.ERR_ARG),
@@ -108,7 +109,7 @@ def test_append_refuses(kw, want):
     (dict(n=-1), spax.ERR_SHAPE), (dict(H=0), spax.ERR_SHAPE), (dict(H=5), spax.ERR_SHAPE),
     (dict(table=None), spax.ERR_ARG), (dict(lens=None), spax.ERR_ARG), (dict(out=None), spax.ERR_ARG),
     (dict(q=None), spax.ERR_ARG), (dict(q=A + 4), spax.ERR_ARG), (dict(out=4 * A + 8), spax.ERR_ARG),
-    (dict(qs=200), spax.ERR_ARG), (dict(qs=258), spax.ERR_ARG), (dict(max_pages=0), spax.ERR_SHAPE),
+    (dict(qs=200), spax.ERR_ARG), (dict(qs=258), spax.ERR_ARG), (dict(qs=1 << 62), spax.ERR_ARG), (dict(max_pages=0), spax.ERR_SHAPE),
     (dict(max_pages=1 << 27), spax.ERR_SHAPE), (dict(out=A), spax.ERR_ARG),
     (dict(out=A + 2048), spax.ERR_ARG),
 ])
@@ -122,6 +123,7 @@ def test_attention_refuses(kw, want):
     (dict(y=None, post=(0, 0, A, None, 1e-5)), spax.ERR_ARG), (dict(y=None, gate=A), spax.ERR_ARG),
     (dict(rs=math.nan), spax.ERR_ARG), (dict(os=math.inf), spax.ERR_ARG),
     (dict(gate=A, gs=63), spax.ERR_ARG), (dict(gate=A, gs=-64), spax.ERR_ARG),
+    (dict(gate=A, gs=1 << 62), spax.ERR_ARG),
     (dict(pre=(2, 0, A, None, 1e-5)), spax.ERR_ARG), (dict(pre=(0, 2, A, None, 1e-5)), spax.ERR_ARG),
     (dict(pre=(0, 0, A, None, -1e-5)), spax.ERR_ARG), (dict(pre=(0, 0, A, None, math.nan)), spax.ERR_ARG),
     (dict(post=(0, 0, A + 2, None, 1e-5)), spax.ERR_ARG), (dict(post=(1, 1, A, A + 1, 1e-5)), spax.ERR_ARG),

@@ -38,9 +38,11 @@ static bool pages_ok(const spax_kv_cache& c, int max_pages) {
   return max_pages >= 1 && (long long)max_pages * c.page_size <= 1 << 30;
 }
 
+constexpr int64_t kMaxStride = 1ll << 32;  // of rows: the last row's offset fits 64 bits
+
 // Rows of `width` floats: aligned for 16-byte accesses, and apart from one another.
 static bool rows_ok(const float* p, int64_t stride, int64_t width, int n) {
-  return p && aligned16(p) && (n <= 1 || (stride >= width && stride % 4 == 0));
+  return p && aligned16(p) && (n <= 1 || (stride >= width && stride <= kMaxStride && stride % 4 == 0));
 }
 
 static bool overlap(const float* a, long long na, const float* b, long long nb) {
@@ -179,7 +181,7 @@ spax_status spax_residual_norm(const float* h, const float* y, int n_tok, int d,
   if (!std::isfinite(res_scale) || !std::isfinite(out_scale)) return SPAX_ERR_ARG;
   if (n_tok == 0) return SPAX_OK;
   if (!h || (!r && !x) || (!y && (h_post || gate))) return SPAX_ERR_ARG;
-  if (gate && gate_stride != 0 && gate_stride < d) return SPAX_ERR_ARG;
+  if (gate && gate_stride != 0 && (gate_stride < d || gate_stride > kMaxStride)) return SPAX_ERR_ARG;
   // outputs may be an input as a whole, and nothing else
   const long long n = (long long)n_tok * d;
   for (const float* o : {static_cast<const float*>(r), static_cast<const float*>(x)}) {
