@@ -556,7 +556,7 @@ typedef struct {
  * L outside [0, max_pages * page_size] is taken as 0, a page outside [0, n_pages) as not seen, and
  * either sets *d_status = SPAX_ERR_INDEX.
  * Products and sums are in fp32 (queries and probabilities enter the matrix instructions in parts
- * that together hold their fp32 value; the sums of e^(s - m) v_j, m up to 8 ln 2 below the largest
+ * that together hold their fp32 value, with an E4M3 cache to within 2^-24 of it; the sums of e^(s - m) v_j, m up to 8 ln 2 below the largest
  * s_j, must not overflow); the split over the length depends on the lengths and the
  * GPU model alone, and its parts are joined in a fixed order: the same bits on every run.
  * Workspace: spax_attention_workspace_bytes() bytes, ZEROED BEFORE FIRST USE; every completed call

@@ -25,15 +25,16 @@
 // pairs of positions that a fragment wants are woven from two rows by byte permutes.
 //
 // Precision: cache elements are exact in bf16 (8-bit ones in fp16). fp32 queries and probabilities
-// enter as parts of 8 bits (three), in fp16 as parts of 11 bits (three of a query; two of a
-// probability, which leave at most 2^-24 of it), smallest first. The matrix instructions add with
-// truncation, so sums over many tiles are kept outside of them. Against 64 bits the outputs are 2e-7
-// to 7e-7 off (2-norm), less than elementary fp32 operations.
+// enter as three parts of 8 bits, which hold them, or in fp16 as two of 11, which leave at most 2^-24
+// of them (half a unit in fp32's last place; a third part of the queries cost 5 to 10% of the time),
+// smallest first. The matrix instructions add with truncation, so sums over many tiles are kept
+// outside of them. Against 64 bits the outputs are 2e-7 to 7e-7 off (2-norm), less than elementary
+// fp32 operations.
 //
 // Measured on B200 (6.55 TB/s is a copy's rate): 131071 positions of 8 key heads 87 to 92 us, 5.8 to 6.2 TB/s; a
-// ragged batch of 64 up to 8192 114 to 118 us, 6.1 to 6.3 TB/s; 33 x 4099 positions of an 8-bit cache 56 us, 4.99
-// TB/s: there the instructions bound it (24 a position, one and a half issued a cycle) and the start
-// and end of a CTA, about 3 and 1 us. One token of 32 heads over 517 positions 8.4 us: launch 2,
+// ragged batch of 64 up to 8192 114 to 118 us, 6.1 to 6.3 TB/s; 33 x 4099 positions of an 8-bit cache 53 us, 5.23
+// TB/s: there its products and their latency bound it, and the start and end of a CTA, about 3 and
+// 1 us. One token of 32 heads over 517 positions 8.4 us: launch 2,
 // start-up 2 (lengths, dealing, page table), copies and tiles 2, the join of nine parts 1.
 #include <type_traits>
 
@@ -54,7 +55,7 @@ struct AttnShape {
   static constexpr int WARPS = WARPS_, THREADS = WARPS * 32;
   static constexpr bool E4M3 = E4M3_;
   static constexpr int ES = E4M3 ? 1 : 2;
-  static constexpr int QP = 3, PP = E4M3 ? 2 : 3;  // parts of a query entry, of a probability
+  static constexpr int PARTS = E4M3 ? 2 : 3;      // of a query entry, of a probability
   static constexpr int ROW = DP * ES;             // bytes of a row of a tile
   static constexpr int CH = ROW / 16;             // 16-byte chunks of a row
   static constexpr int PIECE = TILE * ROW;       // bytes of a tile's keys (or values)
@@ -65,7 +66,7 @@ struct AttnShape {
   // Units of the dealing that a row counts for beside its own: the start-up and the end of a segment
   // take about as long as the copies of 64 KB at a CTA's share of the bandwidth.
   static constexpr int EXTRA = 512 / ROW > 1 ? 512 / ROW : 1;
-  static constexpr int SMEM = RING + KS / 2 * QP * NT * 512;  // and the query's parts
+  static constexpr int SMEM = RING + KS / 2 * PARTS * NT * 512;  // and the query's parts
   static constexpr int OS = DP + 4;               // row stride of the warps' outputs at the join
   static_assert(WARPS * HB * OS * 4 <= RING, "the join's buffer overlays the ring");
   static_assert(CTAS * (SMEM + 3 * 1024) <= 228 * 1024, "shared memory of the resident CTAs");
@@ -512,11 +513,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
           v.x *= up, v.y *= up, v.z *= up, v.w *= up;
           w.x *= up, w.y *= up, w.z *= up, w.w *= up;
 #pragma unroll
-          for (int p = 0; p < S::QP; ++p) {
+          for (int p = 0; p < S::PARTS; ++p) {
             const uint32_t x0 = take_part<S::E4M3>(v.x, v.y), x1 = take_part<S::E4M3>(v.z, v.w);
             const uint32_t y0 = take_part<S::E4M3>(w.x, w.y), y1 = take_part<S::E4M3>(w.z, w.w);
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             qsm + ((pair * S::QP + p) * NT + nt) * 512 + lane * 16),
+                             qsm + ((pair * S::PARTS + p) * NT + nt) * 512 + lane * 16),
                          "r"(x0), "r"(x1), "r"(y0), "r"(y1));
           }
         };
@@ -676,13 +677,13 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int p = S::QP - 1; p >= 0; --p) {
-              const uint4 v = lds128(qsm + ((pair * S::QP + p) * NT + nt) * 512 + lane * 16);
+            for (int p = S::PARTS - 1; p >= 0; --p) {
+              const uint4 v = lds128(qsm + ((pair * S::PARTS + p) * NT + nt) * 512 + lane * 16);
               const bool low = CAREFUL && p > 0;
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
                 float(&d)[4] = acc[mt][nt][p == 0 ? 0 : 1];
-                if (pair == 0 && (p == 0 || p == S::QP - 1))
+                if (pair == 0 && (p == 0 || p == S::PARTS - 1))
                   mma16816<S::E4M3, true>(d, low ? fin[mt][0] : x[mt][0], v.x, v.y);
                 else
                   mma16816<S::E4M3, false>(d, low ? fin[mt][0] : x[mt][0], v.x, v.y);
@@ -725,7 +726,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
           }
         }
 
-        uint32_t pb[MT][NT][S::PP][2];
+        uint32_t pb[MT][NT][S::PARTS][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float s[MT][4], n0 = m[nt][0], n1 = m[nt][1];
@@ -783,7 +784,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
             l[nt][0] += p[0] + p[2];
             l[nt][1] += p[1] + p[3];
 #pragma unroll
-            for (int k = 0; k < S::PP; ++k) {
+            for (int k = 0; k < S::PARTS; ++k) {
               pb[mt][nt][k][0] = transpose8x8(take_part<S::E4M3>(p[0], p[1]));
               pb[mt][nt][k][1] = transpose8x8(take_part<S::E4M3>(p[2], p[3]));
             }
@@ -842,11 +843,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
             for (int nt = 0; nt < NT; ++nt) {
               float t[4];
 #pragma unroll
-              for (int k = S::PP - 1; k >= 0; --k)
+              for (int k = S::PARTS - 1; k >= 0; --k)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                   const uint32_t* a = CAREFUL && k > 0 ? fin[mt] : x[mt];
-                  if (k == S::PP - 1 && mt == 0)
+                  if (k == S::PARTS - 1 && mt == 0)
                     mma16816<S::E4M3, true>(t, a, pb[mt][nt][k][0], pb[mt][nt][k][1]);
                   else
                     mma16816<S::E4M3, false>(t, a, pb[mt][nt][k][0], pb[mt][nt][k][1]);
@@ -1014,7 +1015,8 @@ cudaError_t launch_paged_attention(const AttnLaunch& a, int sm_count, cudaStream
   // are what was fastest of what fits 227 KB and 65536 registers an SM. Measured on B200:
   // - 128-wide bf16, 131071 positions of 8 key heads: 88.9 us; 16 warps an SM (128 registers a
   //   thread) 96 to 98, tiles of 32 positions with 8 warps 94.5;
-  // - 128-wide 8-bit, 33 x 4099 positions: 56.5 us; tiles of 16 positions 68, 16 warps 62 to 63;
+  // - 128-wide 8-bit, 33 x 4099 positions: 53 us (56.5 with three query parts, where tiles of 16
+  //   positions took 68 and 16 warps 62 to 63);
   // - 256-wide bf16: 8 warps of 3 slots 37.6 us on 48 windows of 2048, 6 warps 63, tiles of 32
   //   positions 72; 8-bit, 33 x 4099: tiles of 32 positions 102, of 16 113;
   // - 16 query heads to a key head, ragged batch of 64 up to 8192: bf16 with 12 warps 153, 8 warps 166
