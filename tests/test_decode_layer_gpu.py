@@ -137,3 +137,18 @@ def test_a_layer_decodes(dtype, oracle_lib):
         g.replay()
         assert torch.equal(lay.r2, eager[t]), t
     assert lay.status.item() == 0
+
+
+def test_tensors_of_another_device_than_the_current_one_are_refused(monkeypatch, oracle_lib):
+    """Where the current device is another (here: is said to be), no call takes the tensors."""
+    lay = Layer(0)
+    lay.step()
+    row = lay.qkv.y.view(1, -1)
+    q, k, v = (t.unflatten(1, (-1, D)) for t in row.split([WIDTH, K * D, K * D], 1))
+    monkeypatch.setattr(spax, "_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        spax.spax_kv_append(lay.c, q, k, v, lay.pos, lay.table, lay.status, rope=lay.rope)
+    with pytest.raises(ValueError, match="current device"):
+        spax.spax_paged_attention(lay.c, q, lay.table, lay.len, lay.a, lay.status, lay.ws, scale=1.0)
+    with pytest.raises(ValueError, match="current device"):
+        spax.spax_residual_norm(lay.h, None, None, lay.x1, pre=lay.n1)

@@ -1,11 +1,12 @@
 """spax_paged_attention against the fp64 oracle.
 
 Tolerances, with u = 2^-24 and A the largest sum over the entries of |scale q_i k_i| among the
-positions a head sees. A score is a sum of D exact or once-rounded products taken in at most D steps
-of error 2 u each: it is off by dS = 2 D u A (+ 16 u softcap for the capped form, whose tanh and two
-products are each within a few ulp). A probability's exponent carries the error of the score, of the
-maximum (also dS) and the rounding of its argument (|s - m| <= 2 A, 4 u of it): relative to itself it
-is off by x = 2 dS + 8 u A + 8 u. Numerator and denominator are sums of at most L terms in at most
+positions a head sees. A score is a sum of D products, exact or off by u each (a query entry in two
+fp16 parts), taken in at most D / 2 steps of error 2 u each: it is off by (D + 1) u A, within dS =
+2 D u A (+ 16 u softcap for the capped form, whose tanh and two products are each within a few ulp).
+A probability's exponent carries the error of the score, of the maximum (also dS) and the rounding of
+its argument (|s - m| <= 2 A, 4 u of it): relative to itself it is off by x = 2 dS + 8 u A + 8 u.
+Numerator and denominator are sums of at most L terms in at most
 L / 64 + 160 serial steps (tiles and joins), each 2 u. So
 
     |out - exact| <= (2 x + 4 (L / 64 + 160) u) * sum_j p_j |v_j|,
@@ -262,6 +263,28 @@ def test_non_finite_values_stay_in_their_rows():
     assert torch.isposinf(out[2, 4:, 17]).all()
     out[2, 4:, 17] = ref[0][2, 4:, 17]
     assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+
+
+@pytest.mark.parametrize("H,K,D", [(32, 2, 128), (4, 2, 64), (26, 2, 64), (8, 2, 256), (8, 2, 80)])
+def test_an_infinite_value_is_an_infinite_entry(H, K, D):
+    """In every shape: +-inf at a seen position is +-inf at its entry for the heads that see it, and
+    changes nothing else; a key entry of -inf under positive queries leaves its position out."""
+    case = Case([50, 300], H, K, D, 0, 16, seed=D + H)
+    case.q = case.q.abs()
+    ref = case.run()
+    G = H // K
+    page = int(case.table[1, 2])
+    case.c.v[page, 5, 1, D - 1] = float("inf")
+    case.c.v[page, 6, 0, 0] = -float("inf")
+    out, lse = case.run()
+    assert torch.isposinf(out[1, G:, D - 1]).all() and torch.isneginf(out[1, :G, 0]).all()
+    out[1, G:, D - 1], out[1, :G, 0] = ref[0][1, G:, D - 1], ref[0][1, :G, 0]
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+    case.c.k[page, 5, 1, 3] = case.c.k[page, 6, 0, 3] = -float("inf")
+    case.c.v[page, 5, 1, D - 1] = case.c.v[page, 6, 0, 0] = 0.0
+    out, lse = case.run()
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    case.check(out, lse)
 
 
 def test_scores_of_minus_infinity():
