@@ -123,9 +123,9 @@ def test_one_sequence_split_over_its_length(lens, H, K, D, dtype):
 @pytest.mark.parametrize("H,K,D,dtype", [(8, 1, 80, 0), (8, 1, 112, 1), (5, 1, 48, 0), (16, 2, 96, 0),
                                          (6, 1, 176, 1), (12, 1, 16, 0), (16, 1, 112, 1)])
 def test_heads_that_no_warp_holds_alone_are_joined(H, K, D, dtype):
-    """Rows of many parts, joined in two steps by threads of several warps to a head, often enough
+    """Rows of many parts, joined in one or two steps by threads of several warps to a head, often enough
     that their order differs."""
-    for n in (1100, 4000, 17 * 64):
+    for n in (1100, 4000, 17 * 64, 60 * 64):
         case = Case([n, 5, n - 1], H, K, D, dtype, 32, seed=n)
         first = case.run()
         case.check(*first)

@@ -43,7 +43,7 @@
 namespace spax {
 
 constexpr int kUnit = 64;  // positions in a unit of work, starting at a multiple of 64
-constexpr int kJoin = 16;  // parts that are joined in one step
+constexpr int kJoin = 32;  // parts that are joined in one step (52 take 0.7 to 2 us less in two)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Shapes of one instance: head_dim padded to DP, NT blocks of 8 query heads, tiles of 16 MT positions,
@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       // into the slot of the group's first: two short reads in place of one long one.
       int group = n;
       if (n > kJoin)
-        for (group = kJoin / 2; group * group < n;) ++group;
+        for (group = 8; group * group < n;) ++group;
       const int k0 = (b - b0) / group * group, groups = (n + group - 1) / group;
       bool last = arrive(g.tickets + slot_of(k0), min(group, n - k0), &is_last);
       if (last) {
