@@ -265,6 +265,22 @@ def test_non_finite_values_stay_in_their_rows():
     assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("H,K,D", [(32, 2, 128), (4, 2, 64), (8, 2, 256)])
+@pytest.mark.parametrize("entry", [float("inf"), -float("inf")])
+def test_an_infinite_query_is_a_head_of_nan(entry, H, K, D, dtype):
+    """Its head alone, and nothing where the sequence is empty."""
+    case = Case([1, 300, 0], H, K, D, dtype, 16, seed=D + H)
+    case.q[:, 2, 7] = entry
+    out, lse = case.run()
+    assert torch.isnan(out[:2, 2]).all() and torch.isnan(lse[:2, 2]).all()
+    assert torch.all(out[2] == 0) and torch.isneginf(lse[2]).all()
+    case.q[:, 2, 7] = 0.0  # the oracle's other heads do not read it
+    other = case.run()
+    out[:, 2], lse[:, 2] = other[0][:, 2], other[1][:, 2]
+    case.check(out, lse)
+
+
 @pytest.mark.parametrize("H,K,D", [(32, 2, 128), (4, 2, 64), (26, 2, 64), (8, 2, 256), (8, 2, 80)])
 def test_an_infinite_value_is_an_infinite_entry(H, K, D):
     """In every shape: +-inf at a seen position is +-inf at its entry for the heads that see it, and
