@@ -34,7 +34,7 @@
 // Measured on B200 (6.55 TB/s is a copy's rate): 131071 positions of 8 key heads 87 to 92 us, 5.8 to 6.2 TB/s; a
 // ragged batch of 64 up to 8192 114 to 118 us, 6.1 to 6.3 TB/s; 33 x 4099 positions of an 8-bit cache 53 us, 5.23
 // TB/s: there its products and their latency bound it, and the start and end of a CTA, about 3 and
-// 1 us. One token of 32 heads over 517 positions 8.4 us: launch 2,
+// 1 us. One token of 32 heads over 517 positions 8.2 us: launch 2,
 // start-up 2 (lengths, dealing, page table), copies and tiles 2, the join of nine parts 1.
 #include <type_traits>
 
@@ -43,7 +43,7 @@
 namespace spax {
 
 constexpr int kUnit = 64;  // positions in a unit of work, starting at a multiple of 64
-constexpr int kJoin = 32;  // parts that are joined in one step (52 take 0.7 to 2 us less in two)
+constexpr int kJoin = 16;  // parts that are joined in one step (32 of 256-wide heads: 15.7 us, in two 13.1)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Shapes of one instance: head_dim padded to DP, NT blocks of 8 query heads, tiles of 16 MT positions,
@@ -63,6 +63,9 @@ struct AttnShape {
   static constexpr int RING = WARPS * SLOTS * PIECE;
   static_assert(SLOTS % 2 == 1 && SLOTS >= 3);
   static constexpr int KS = DP / 16;              // k steps of a score
+  // Units of the shortest run, which has a tile for each warp (8-bit 128-wide, 512 positions: 8.0 us in
+  // runs of 2 units, 9.2 in runs of 1, whose second pair of warps had nothing).
+  static constexpr int LEAST = (WARPS * TILE + kUnit - 1) / kUnit;
   // Units of the dealing that a row counts for beside its own: the start-up and the end of a segment
   // take about as long as the copies of 64 KB at a CTA's share of the bandwidth.
   static constexpr int EXTRA = 512 / ROW > 1 ? 512 / ROW : 1;
@@ -222,55 +225,82 @@ __device__ __forceinline__ void put_row(const AttnArgs& g, float2* ml, int slot,
   }
 }
 
-// Joins n parts of a row, the slots of which slot_of gives, in their order: a thread takes the
-// maxima, sums and entries of N parts at a time, all in flight at once. A slot that is joined to may
-// be one of the parts: an entry is read and written by one thread alone, while the maximum and sum,
-// which several threads read, go to another array (the second step's).
-template <class S, int N, class F>
-__device__ __forceinline__ void join(const AttnArgs& g, const float2* from_ml, int heads, int n, F slot_of,
+// The slots of a row's parts in their order.
+struct Parts {
+  int first, next, step;
+  __device__ __forceinline__ long long slot(int k) const { return k == 0 ? first : next + k * step; }
+};
+
+// Joins n parts of a row in their order: a thread takes the maxima, sums and entries of N parts for E
+// of its quads at a time, all in flight at once, since each go costs a round trip to L2. A slot that is
+// joined to may be one of the parts: an entry is read and written by one thread alone, while the
+// maximum and sum, which several threads read, go to another array (the second step's).
+template <class S, int N, int E>
+__device__ __forceinline__ void join(const AttnArgs& g, const float2* from_ml, int heads, int n, Parts parts,
                                      int to, long long at) {
-  const int quads = g.a.cache.head_dim / 4;
-  for (int e = threadIdx.x; e < heads * quads; e += S::THREADS) {
-    const int h = e / quads, d = (e - h * quads) * 4;
-    float4 v = make_float4(0, 0, 0, 0);
-    float M = -INFINITY, L = 0.0f;
+  const int quads = g.a.cache.head_dim / 4, all = heads * quads;
+  for (int e0 = threadIdx.x; e0 < all; e0 += E * S::THREADS) {
+    int h[E], d[E];
+    float4 v[E];
+    float M[E], L[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const int e = e0 + j * S::THREADS < all ? e0 + j * S::THREADS : e0;  // past the end: its first again
+      h[j] = e / quads, d[j] = (e - h[j] * quads) * 4;
+      v[j] = make_float4(0, 0, 0, 0);
+      M[j] = -INFINITY, L[j] = 0.0f;
+    }
     for (int k = 0; k < n; k += N) {
-      float4 t[N];
-      float2 ml[N];
+      float4 t[E][N];
+      float2 ml[E][N];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        ml[i] = make_float2(-INFINITY, 0.0f);
-        t[i] = make_float4(0, 0, 0, 0);
-        if (k + i < n) {
-          const long long slot = slot_of(k + i);
-          ml[i] = __ldcg(from_ml + slot * S::HB + h);
-          t[i] = __ldcg(reinterpret_cast<const float4*>(g.part + (slot * S::HB + h) * S::DP + d));
+        const long long slot = parts.slot(k + i);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          ml[j][i] = make_float2(-INFINITY, 0.0f);
+          t[j][i] = make_float4(0, 0, 0, 0);
+          if (k + i < n) {
+            ml[j][i] = __ldcg(from_ml + slot * S::HB + h[j]);
+            t[j][i] = __ldcg(reinterpret_cast<const float4*>(g.part + (slot * S::HB + h[j]) * S::DP + d[j]));
+          }
         }
       }
-      float top = M;
 #pragma unroll
-      for (int i = 0; i < N; ++i) top = fmaxf(top, ml[i].x);  // drops a NaN: its sum is NaN too
-      const float fade = M == -INFINITY ? 0.0f : exp2_ftz(M - top);
-      L *= fade;
-      v.x *= fade, v.y *= fade, v.z *= fade, v.w *= fade;
+      for (int j = 0; j < E; ++j) {
+        float top = M[j];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float f = ml[i].x == -INFINITY ? 0.0f : exp2_ftz(ml[i].x - top);
-        L += f * ml[i].y;
-        v.x += f * t[i].x, v.y += f * t[i].y, v.z += f * t[i].z, v.w += f * t[i].w;
+        for (int i = 0; i < N; ++i) top = fmaxf(top, ml[j][i].x);  // drops a NaN: its sum is NaN too
+        const float fade = M[j] == -INFINITY ? 0.0f : exp2_ftz(M[j] - top);
+        L[j] *= fade;
+        v[j].x *= fade, v[j].y *= fade, v[j].z *= fade, v[j].w *= fade;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float f = ml[j][i].x == -INFINITY ? 0.0f : exp2_ftz(ml[j][i].x - top);
+          L[j] += f * ml[j][i].y;
+          v[j].x += f * t[j][i].x, v[j].y += f * t[j][i].y, v[j].z += f * t[j][i].z, v[j].w += f * t[j][i].w;
+        }
+        M[j] = top;
       }
-      M = top;
     }
-    put_row<S>(g, g.part_ml2, to, at, h, d, v, M, L);
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (e0 + j * S::THREADS < all) put_row<S>(g, g.part_ml2, to, at, h[j], d[j], v[j], M[j], L[j]);
   }
 }
-template <class S, class F>
-__device__ __forceinline__ void join(const AttnArgs& g, const float2* from_ml, int heads, int n, F slot_of,
-                                     int to, long long at) {
+template <class S>
+__device__ __forceinline__ void join(const AttnArgs& g, const float2* from_ml, int heads, int n, Parts parts, int to,
+                                     long long at) {
+  // Two quads at a time where a row has more than one for each thread; 16 parts of one fill the
+  // registers. Measured on B200, 8 query heads, 512 positions (8 parts): 256-wide 10.6 us, 11.7 with
+  // 16 places for parts and one quad at a time; 128-wide 7.6 and 9.1.
+  constexpr int E = S::HB * S::DP / 4 > S::THREADS ? 2 : 1;
   if (n <= 4)
-    join<S, 4>(g, from_ml, heads, n, slot_of, to, at);
+    join<S, 4, E>(g, from_ml, heads, n, parts, to, at);
+  else if (n <= 8)
+    join<S, 8, E>(g, from_ml, heads, n, parts, to, at);
   else
-    join<S, 16>(g, from_ml, heads, n, slot_of, to, at);
+    join<S, 16, 1>(g, from_ml, heads, n, parts, to, at);
 }
 
 template <class S>
@@ -338,7 +368,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
   if (U > 0) {
     const int rows = rows_of_seq * total([](int u) { return u > 0; });
     if (2 * rows <= (int)gridDim.x) {
-      run = U == B ? 1 : (U + B - 1) / B;
+      run = max(S::LEAST, (U + B - 1) / B);
       // a run may be this much longer than equal runs before their row ends cost less
       const int most = run + max(6, run / 16);
       const int more = few ? max(1, run / 16) : (most - run) / 2;
@@ -934,19 +964,19 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       const int slot0 = 2 * b0 + (run || row_begin <= start_of(b0) ? 0 : 1);
       const long long at = (long long)seq * g.a.n_heads + head0;
       auto slot_of = [&](int k) { return k == 0 ? slot0 : 2 * (b0 + k); };
-      // In one step up to kJoin parts; else groups of about sqrt(n) first, each by its own last CTA,
-      // into the slot of the group's first: two short reads in place of one long one.
-      int group = n;
-      if (n > kJoin)
-        for (group = 8; group * group < n;) ++group;
+      // In one step up to kJoin parts; else groups first, each by its own last CTA, into the slot of
+      // the group's first: two short reads in place of a long one. A group of 8 or 16 is read in one
+      // go, and so are the up to 16 groups (8 query heads: 128 parts 12.6 us, 13.9 in groups of 12; 444
+      // parts 16.2 in groups of 32, 17.5 in groups of 22).
+      const int group = n <= kJoin ? n : n <= 128 ? 8 : n <= 256 ? 16 : 32;
       const int k0 = (b - b0) / group * group, groups = (n + group - 1) / group;
       bool last = arrive(g.tickets + slot_of(k0), min(group, n - k0), &is_last);
       if (last) {
-        join<S>(g, g.part_ml, heads, min(group, n - k0), [&](int i) { return slot_of(k0 + i); },
+        join<S>(g, g.part_ml, heads, min(group, n - k0), {slot_of(k0), 2 * (b0 + k0), 2},
                 groups == 1 ? -1 : slot_of(k0), at);
         if (groups > 1) {
           last = arrive(g.tickets2 + slot0, groups, &is_last);
-          if (last) join<S>(g, g.part_ml2, heads, groups, [&](int i) { return slot_of(i * group); }, -1, at);
+          if (last) join<S>(g, g.part_ml2, heads, groups, {slot0, 2 * b0, 2 * group}, -1, at);
         }
       }
     }
