@@ -957,6 +957,7 @@ def run_decode_layer(args, dev):
         table = torch.randperm(pages, device=dev).int().view(1, pages)
         pos = torch.full((1,), ctx - 1, dtype=torch.int32, device=dev)
         lens = torch.full((1,), ctx, dtype=torch.int32, device=dev)
+        torch.cuda.synchronize()  # the caches and the table, before `stream` reads them
 
         def between(t):  # qkv's row -> the attention's output
             kv = caches[t % n_cache]
