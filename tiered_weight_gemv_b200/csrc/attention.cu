@@ -31,8 +31,8 @@
 // outside of them. Against 64 bits the outputs are 2e-7 to 7e-7 off (2-norm), less than elementary
 // fp32 operations.
 //
-// Measured on B200 (6.55 TB/s is a copy's rate): 131071 positions of 8 key heads 87 to 92 us, 5.8 to 6.2 TB/s; a
-// ragged batch of 64 up to 8192 114 to 118 us, 6.1 to 6.3 TB/s; 33 x 4099 positions of an 8-bit cache 53 us, 5.23
+// Measured on B200 (6.55 TB/s is a copy's rate): 131071 positions of 8 key heads 87 to 90 us, 6.0 to 6.2 TB/s; a
+// ragged batch of 64 up to 8192 113 to 116 us, 6.2 to 6.4 TB/s; 33 x 4099 positions of an 8-bit cache 52 us, 5.4
 // TB/s: there its products and their latency bound it, and the start and end of a CTA, about 3 and
 // 1 us. One token of 32 heads over 517 positions 8.2 us: launch 2,
 // start-up 2 (lengths, dealing, page table), copies and tiles 2, the join of nine parts 1.
@@ -132,9 +132,18 @@ __device__ __forceinline__ uint32_t take_part(float& x, float& y) {
   return d;
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? 16 : 0));
+// The cache is read once a token and is the first to leave L2 again. Else 67 MB of it push out what the
+// projections around the call keep there (their code, the activations, their workspaces): a
+// Llama-2-7B layer at a context of 4096 takes 109 us a token then and 96 so, the attention alone
+// 116 and 113 (ragged batch of 64 up to 8192).
+__device__ __forceinline__ uint64_t evict_first() {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0), "l"(policy));
 }
 
 // Pairs of bf16 elements with an infinity replaced by the largest finite value: what the lower parts
@@ -626,6 +635,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       // fragments' loads spread over the banks: keys with rows of unlike parity in different halves,
       // values with pairs of rows apart.
       const long long step = RPI * C.token_stride * S::ES;
+      const uint64_t policy = evict_first();
       auto issue = [&](const Place& at, bool real_tile, bool keys, int slot) {
         if (real_tile) {
           const uint32_t piece = ring + slot * S::PIECE;
@@ -641,7 +651,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
               const uint8_t* src = pool + at.off[mt];
 #pragma unroll
               for (int k = 0; k < 16 / RPI; ++k) {
-                cp16(spot(mt * 16 + k * RPI + row0), src, true);
+                cp16(spot(mt * 16 + k * RPI + row0), src, true, policy);
                 src += step;
               }
             }
@@ -650,7 +660,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
             for (int k = 0; k < TILE / RPI; ++k) {
               const long long row_off = __shfl_sync(~0u, at.off[0], k * RPI + row0);
               const bool real = row_off >= 0 && ch < chunks;
-              cp16(spot(k * RPI + row0), pool + (real ? row_off + ch * 16 : 0), real);
+              cp16(spot(k * RPI + row0), pool + (real ? row_off + ch * 16 : 0), real, policy);
             }
           }
         }
@@ -1042,7 +1052,8 @@ cudaError_t launch_paged_attention(const AttnLaunch& a, int sm_count, cudaStream
   const int dp = padded_dim(a.cache.head_dim), nt = head_blocks(g.row_heads, a.cache.head_dim);
   const bool e = a.cache.dtype == SPAX_KV_E4M3;
   // The shape by head_dim (padded), type and query heads to a key head; tiles, warps, slots and CTAs
-  // are what was fastest of what fits 227 KB and 65536 registers an SM. Measured on B200:
+  // are what was fastest of what fits 227 KB and 65536 registers an SM. Measured on B200, before the
+  // copies left L2 first (1 to 3% less with it):
   // - 128-wide bf16, 131071 positions of 8 key heads: 88.9 us; 16 warps an SM (128 registers a
   //   thread) 96 to 98, tiles of 32 positions with 8 warps 94.5;
   // - 128-wide 8-bit, 33 x 4099 positions: 53 us (56.5 with three query parts, where tiles of 16
