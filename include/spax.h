@@ -582,6 +582,15 @@ spax_status spax_paged_attention(const spax_kv_cache* h_cache, const float* d_q,
 size_t spax_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim);
 
 /*
+ * Host-only, no CUDA call: the CTAs that spax_paged_attention launches on a GPU with sm_count SMs for
+ * tables of max_positions (max_pages * page_size) positions a sequence, by the rule that the call uses,
+ * and the workspace bytes there. Requires what the call requires of these arguments, n_seq >= 1.
+ */
+spax_status spax_attention_plan_sms(int n_seq, int n_heads, int n_kv_heads, int head_dim, int kv_dtype,
+                                    int64_t max_positions, int window, int sm_count, int32_t* ctas,
+                                    size_t* ws_bytes);
+
+/*
  * A norm over the d entries of a row z. RMS: z / sqrt(mean(z^2) + eps). LAYER: (z - mean(z)) /
  * sqrt(mean((z - mean(z))^2) + eps). Then times d_weight and plus d_bias ([d] of w_dtype on the
  * device; NULL: none). eps >= 0.

@@ -113,6 +113,22 @@ size_t spax_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim)
   return sms < 1 ? 0 : attention_ws_bytes(n_heads, n_kv_heads, head_dim, sms);
 }
 
+spax_status spax_attention_plan_sms(int n_seq, int n_heads, int n_kv_heads, int head_dim, int kv_dtype,
+                                    int64_t max_positions, int window, int sm_count, int32_t* ctas,
+                                    size_t* ws_bytes) {
+  if (kv_dtype != SPAX_KV_BF16 && kv_dtype != SPAX_KV_E4M3) return SPAX_ERR_ARG;
+  if (window < 0 || sm_count < 1) return SPAX_ERR_ARG;
+  if (n_seq < 1 || n_seq > 65535 || n_heads < 1 || n_heads > 65535) return SPAX_ERR_SHAPE;
+  if (n_kv_heads < 1 || n_heads % n_kv_heads != 0) return SPAX_ERR_SHAPE;
+  if (head_dim < 16 || head_dim > 256 || head_dim % 16 != 0) return SPAX_ERR_SHAPE;
+  if (max_positions < 1 || max_positions > 1 << 30) return SPAX_ERR_SHAPE;
+  if (ctas)
+    *ctas = attention_ctas(n_seq, n_heads, n_kv_heads, head_dim, kv_dtype == SPAX_KV_E4M3, max_positions, window,
+                           sm_count);
+  if (ws_bytes) *ws_bytes = attention_ws_bytes(n_heads, n_kv_heads, head_dim, sm_count);
+  return SPAX_OK;
+}
+
 spax_status spax_paged_attention(const spax_kv_cache* h_cache, const float* q, int64_t q_stride,
                                  int n_seq, int n_heads, const int32_t* page_table, int max_pages,
                                  const int32_t* seq_lens, const spax_attn_params* h_params,

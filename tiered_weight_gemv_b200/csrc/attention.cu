@@ -1015,6 +1015,22 @@ size_t attention_ws_bytes(int n_heads, int n_kv_heads, int head_dim, int sm_coun
   return slots * hb * (padded_dim(head_dim) * 4 + 16) + ((slots * 8 + 255) & ~size_t(255));
 }
 
+// CTAs of a call whose tables hold max_pos positions a sequence: a wave, or fewer where the units that
+// there can be are fewer. In 64 bits: a window of 2^31 - 1 is a common way to ask for none.
+static int grid_ctas(long long rows, long long max_pos, int window, int wave) {
+  const long long seen = (long long)window + kUnit;
+  const long long longest = window > 0 && seen < max_pos ? seen : max_pos;
+  const long long units = rows * ((longest + kUnit - 1) / kUnit);
+  return (int)(units < wave ? units : wave);
+}
+
+template <class S>
+static int shape_ctas(int n_seq, int n_kv_heads, int row_heads, long long max_pos, int window, int sm_count) {
+  static_assert(S::CTAS <= kMaxCtas, "workspace slots");
+  const int blocks = (row_heads + S::HB - 1) / S::HB;
+  return grid_ctas((long long)n_seq * n_kv_heads * blocks, max_pos, window, S::CTAS * sm_count);
+}
+
 template <class S>
 static cudaError_t launch_shape(AttnArgs g, int sm_count, cudaStream_t stream) {
   const void* f = reinterpret_cast<const void*>(attention_kernel<S>);
@@ -1027,14 +1043,41 @@ static cudaError_t launch_shape(AttnArgs g, int sm_count, cudaStream_t stream) {
   g.part = reinterpret_cast<float*>(static_cast<uint8_t*>(g.a.ws) + ((slots * 8 + 255) & ~255ll));
   g.part_ml = reinterpret_cast<float2*>(g.part + slots * S::HB * S::DP);
   g.part_ml2 = g.part_ml + slots * S::HB;
-  long long longest = (long long)g.a.max_pages * g.a.cache.page_size;
-  if (g.a.prm.window > 0 && g.a.prm.window + kUnit < longest) longest = g.a.prm.window + kUnit;
-  const long long units = (long long)g.a.n_seq * g.a.cache.n_kv_heads * g.blocks *
-                          ((longest + kUnit - 1) / kUnit);
-  static_assert(S::CTAS <= kMaxCtas, "workspace slots");
-  const long long wave = (long long)S::CTAS * sm_count;
-  return launch_pdl(attention_kernel<S>, dim3((unsigned)(units < wave ? units : wave)),
-                    dim3(S::THREADS), (size_t)S::SMEM, stream, g);
+  const int ctas = shape_ctas<S>(g.a.n_seq, g.a.cache.n_kv_heads, g.row_heads,
+                                 (long long)g.a.max_pages * g.a.cache.page_size, g.a.prm.window, sm_count);
+  return launch_pdl(attention_kernel<S>, dim3(ctas), dim3(S::THREADS), (size_t)S::SMEM, stream, g);
+}
+
+// Calls f with the shape by head_dim (padded), type and query heads to a key head; tiles, warps, slots
+// and CTAs are what was fastest of what fits 227 KB and 65536 registers an SM. Measured on B200, before
+// the copies left L2 first (1 to 3% less with it):
+// - 128-wide bf16, 131071 positions of 8 key heads: 88.9 us; 16 warps an SM (128 registers a
+//   thread) 96 to 98, tiles of 32 positions with 8 warps 94.5;
+// - 128-wide 8-bit, 33 x 4099 positions: 53 us (56.5 with three query parts, where tiles of 16
+//   positions took 68 and 16 warps 62 to 63);
+// - 256-wide bf16: 8 warps of 3 slots 37.6 us on 48 windows of 2048, 6 warps 63, tiles of 32
+//   positions 72; 8-bit, 33 x 4099: tiles of 32 positions 102, of 16 113;
+// - 16 query heads to a key head, ragged batch of 64 up to 8192: bf16 with 12 warps 153, 8 warps 166
+//   (one sequence alone prefers 8: 40 to 48); 8-bit tiles of 32 positions 89, of 16 99.
+template <class F>
+static auto with_shape(int head_dim, int row_heads, bool e4m3, F f) {
+  const int dp = padded_dim(head_dim), nt = head_blocks(row_heads, head_dim);
+  if (dp == 64 && nt == 1)
+    return e4m3 ? f(AttnShape<64, true, 1, 2, 4, 5, 3>()) : f(AttnShape<64, false, 1, 2, 4, 3, 3>());
+  if (dp == 64) return e4m3 ? f(AttnShape<64, true, 2, 2, 4, 3, 3>()) : f(AttnShape<64, false, 2, 2, 4, 3, 3>());
+  if (dp == 128 && nt == 1)
+    return e4m3 ? f(AttnShape<128, true, 1, 2, 4, 3, 3>()) : f(AttnShape<128, false, 1, 1, 4, 3, 3>());
+  if (dp == 128)
+    return e4m3 ? f(AttnShape<128, true, 2, 2, 4, 3, 2>()) : f(AttnShape<128, false, 2, 1, 4, 3, 3>());
+  return e4m3 ? f(AttnShape<256, true, 1, 2, 4, 3, 2>()) : f(AttnShape<256, false, 1, 1, 4, 3, 2>());
+}
+
+int attention_ctas(int n_seq, int n_heads, int n_kv_heads, int head_dim, bool e4m3, long long max_pos,
+                   int window, int sm_count) {
+  const int row_heads = n_heads / n_kv_heads;
+  return with_shape(head_dim, row_heads, e4m3, [&](auto shape) {
+    return shape_ctas<decltype(shape)>(n_seq, n_kv_heads, row_heads, max_pos, window, sm_count);
+  });
 }
 
 cudaError_t launch_paged_attention(const AttnLaunch& a, int sm_count, cudaStream_t stream) {
@@ -1049,33 +1092,8 @@ cudaError_t launch_paged_attention(const AttnLaunch& a, int sm_count, cudaStream
   g.page_shift = s - 1;
   g.page_mul = d == 1 ? 0 : (uint32_t)((1ull << (31 + s)) / d + 1);
   g.page16 = d % 16 == 0;
-  const int dp = padded_dim(a.cache.head_dim), nt = head_blocks(g.row_heads, a.cache.head_dim);
-  const bool e = a.cache.dtype == SPAX_KV_E4M3;
-  // The shape by head_dim (padded), type and query heads to a key head; tiles, warps, slots and CTAs
-  // are what was fastest of what fits 227 KB and 65536 registers an SM. Measured on B200, before the
-  // copies left L2 first (1 to 3% less with it):
-  // - 128-wide bf16, 131071 positions of 8 key heads: 88.9 us; 16 warps an SM (128 registers a
-  //   thread) 96 to 98, tiles of 32 positions with 8 warps 94.5;
-  // - 128-wide 8-bit, 33 x 4099 positions: 53 us (56.5 with three query parts, where tiles of 16
-  //   positions took 68 and 16 warps 62 to 63);
-  // - 256-wide bf16: 8 warps of 3 slots 37.6 us on 48 windows of 2048, 6 warps 63, tiles of 32
-  //   positions 72; 8-bit, 33 x 4099: tiles of 32 positions 102, of 16 113;
-  // - 16 query heads to a key head, ragged batch of 64 up to 8192: bf16 with 12 warps 153, 8 warps 166
-  //   (one sequence alone prefers 8: 40 to 48); 8-bit tiles of 32 positions 89, of 16 99.
-  if (dp == 64 && nt == 1)
-    return e ? launch_shape<AttnShape<64, true, 1, 2, 4, 5, 3>>(g, sm_count, stream)
-             : launch_shape<AttnShape<64, false, 1, 2, 4, 3, 3>>(g, sm_count, stream);
-  if (dp == 64)
-    return e ? launch_shape<AttnShape<64, true, 2, 2, 4, 3, 3>>(g, sm_count, stream)
-             : launch_shape<AttnShape<64, false, 2, 2, 4, 3, 3>>(g, sm_count, stream);
-  if (dp == 128 && nt == 1)
-    return e ? launch_shape<AttnShape<128, true, 1, 2, 4, 3, 3>>(g, sm_count, stream)
-             : launch_shape<AttnShape<128, false, 1, 1, 4, 3, 3>>(g, sm_count, stream);
-  if (dp == 128)
-    return e ? launch_shape<AttnShape<128, true, 2, 2, 4, 3, 2>>(g, sm_count, stream)
-             : launch_shape<AttnShape<128, false, 2, 1, 4, 3, 3>>(g, sm_count, stream);
-  return e ? launch_shape<AttnShape<256, true, 1, 2, 4, 3, 2>>(g, sm_count, stream)
-           : launch_shape<AttnShape<256, false, 1, 1, 4, 3, 2>>(g, sm_count, stream);
+  return with_shape(a.cache.head_dim, g.row_heads, a.cache.dtype == SPAX_KV_E4M3,
+                    [&](auto shape) { return launch_shape<decltype(shape)>(g, sm_count, stream); });
 }
 
 }  // namespace spax

@@ -93,6 +93,9 @@ struct AttnLaunch {
   int n_seq, n_heads, max_pages;
 };
 size_t attention_ws_bytes(int n_heads, int n_kv_heads, int head_dim, int sm_count);
+// The launch's CTAs; max_pos is the positions that a sequence's row of the page table holds.
+int attention_ctas(int n_seq, int n_heads, int n_kv_heads, int head_dim, bool e4m3, long long max_pos,
+                   int window, int sm_count);
 cudaError_t launch_paged_attention(const AttnLaunch& a, int sm_count, cudaStream_t stream);
 
 struct NormLaunch {

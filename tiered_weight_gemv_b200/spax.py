@@ -116,6 +116,7 @@ _SIGS = {
                         _P], _I),
     "spax_paged_attention": ([_P, _P, _L, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _Z, _P], _I),
     "spax_attention_workspace_bytes": ([_I, _I, _I], _Z),
+    "spax_attention_plan_sms": ([_I, _I, _I, _I, _I, _L, _I, _I, _P, _P], _I),
     "spax_residual_norm": ([_P, _P, _I, _I, _P, _P, _L, _F, _F, _P, _P, _P, _P], _I),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -642,6 +643,16 @@ def spax_kv_append(cache: KvCache, q, k: torch.Tensor, v: torch.Tensor, pos: tor
 
 def spax_attention_workspace_bytes(n_heads: int, n_kv_heads: int, head_dim: int) -> int:
     return int(_lib.spax_attention_workspace_bytes(n_heads, n_kv_heads, head_dim))
+
+
+def spax_attention_plan_sms(n_seq: int, n_heads: int, n_kv_heads: int, head_dim: int, kv_dtype: int,
+                            max_positions: int, window: int, sm_count: int):
+    """(CTAs, workspace bytes) of spax_paged_attention on a GPU with sm_count SMs; no CUDA call."""
+    ctas, ws = ctypes.c_int32(), ctypes.c_size_t()
+    _check("spax_attention_plan_sms", _lib.spax_attention_plan_sms(
+        n_seq, n_heads, n_kv_heads, head_dim, kv_dtype, max_positions, window, sm_count,
+        ctypes.byref(ctas), ctypes.byref(ws)))
+    return ctas.value, ws.value
 
 
 def alloc_attention_workspace(cache: KvCache, n_heads: int) -> torch.Tensor:
