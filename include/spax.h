@@ -557,9 +557,11 @@ typedef struct {
  * cache past L, and outside the window, are not read: what they hold cannot matter.
  * L outside [0, max_pages * page_size] is taken as 0, a page outside [0, n_pages) as not seen, and
  * either sets *d_status = SPAX_ERR_INDEX.
- * Products and sums are in fp32 (queries and probabilities enter the matrix instructions in parts
- * that together hold their fp32 value, with an E4M3 cache to within 2^-24 of it; the sums of e^(s - m) v_j, m up to 8 ln 2 below the largest
- * s_j, must not overflow); the split over the length depends on the lengths and the
+ * Products and sums are in fp32; queries and probabilities enter the matrix instructions in parts. With
+ * a BF16 cache the parts hold the fp32 value. With an E4M3 cache they are off by at most 2^-23 of it, or
+ * where that is more by 2^-51 of the head's largest entry (that being at least 2^-86) and 2^-49 of the
+ * head's largest probability. The sums of e^(s - m) v_j, m up to 8 ln 2 below the largest s_j, must not
+ * overflow. The split over the length depends on the lengths and the
  * GPU model alone, and its parts are joined in a fixed order: the same bits on every run.
  * Workspace: spax_attention_workspace_bytes() bytes, ZEROED BEFORE FIRST USE; every completed call
  * leaves its counters at zero (zero it again after a device error). Calls that share a workspace

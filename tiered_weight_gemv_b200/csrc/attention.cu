@@ -25,10 +25,15 @@
 // pairs of positions that a fragment wants are woven from two rows by byte permutes.
 //
 // Precision: cache elements are exact in bf16 (8-bit ones in fp16). fp32 queries and probabilities
-// enter as three parts of 8 bits, which hold them, or in fp16 as two of 11, which leave at most 2^-24
-// of them (half a unit in fp32's last place; a third part of the queries cost 5 to 10% of the time),
-// smallest first. The matrix instructions add with truncation, so sums over many tiles are kept
-// outside of them. Against 64 bits the outputs are 2e-7 to 7e-7 off (2-norm), less than elementary
+// enter as three parts of 8 bits, which hold them, or in fp16 as two of 11. A remainder of 12 bits can
+// meet the second of these, which then leaves 2^-23 of the value (a unit in fp32's last place; a third
+// part of the queries cost 5 to 10% of the time). fp16 ends at 2^-24, so a head's largest query is
+// brought below 2^15, probabilities are lifted by 2^12, and the second parts by another 2^12, in sums
+// of their own: entries down to 2^-28 of the head's largest, and probabilities down to 2^-26 of the
+// largest, are within 2^-23 of themselves, and smaller ones within 2^-51 and 2^-49 of the largest (0 to
+// 1.5% of the time, 33 x 4099 positions 51.3 -> 52.0 us; without the second lift entries from 2^-17 of
+// the largest on lose bits). The matrix instructions add with truncation, so sums over many tiles are
+// kept outside of them. Against 64 bits the outputs are 2e-7 to 7e-7 off (2-norm), less than elementary
 // fp32 operations.
 //
 // Measured on B200 (6.55 TB/s is a copy's rate): 131071 positions of 8 key heads 87 to 90 us, 6.0 to 6.2 TB/s; a
@@ -44,6 +49,7 @@ namespace spax {
 
 constexpr int kUnit = 64;  // positions in a unit of work, starting at a multiple of 64
 constexpr int kJoin = 16;  // parts that are joined in one step (32 of 256-wide heads: 15.7 us, in two 13.1)
+constexpr float kLow = 4096.0f;  // of the fp16 parts
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Shapes of one instance: head_dim padded to DP, NT blocks of 8 query heads, tiles of 16 MT positions,
@@ -56,6 +62,7 @@ struct AttnShape {
   static constexpr bool E4M3 = E4M3_;
   static constexpr int ES = E4M3 ? 1 : 2;
   static constexpr int PARTS = E4M3 ? 2 : 3;      // of a query entry, of a probability
+  static constexpr float LOW = E4M3 ? kLow : 1.0f;  // the lower parts are held times this
   static constexpr int ROW = DP * ES;             // bytes of a row of a tile
   static constexpr int CH = ROW / 16;             // 16-byte chunks of a row
   static constexpr int PIECE = TILE * ROW;       // bytes of a tile's keys (or values)
@@ -115,15 +122,21 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t* low, uint32_
       : "r"(w));
 }
 
-// (x, y) as a pair in the matrix type, and what the pair leaves of them.
+__device__ __forceinline__ void scale_pair(float& x, float& y, float by) {
+  const f2 r = ffma2(f2{x, y}, f2{by, by}, f2{0.0f, 0.0f});
+  x = r.x, y = r.y;
+}
+
+// (x, y) as a pair in the matrix type, and what the pair leaves of them (times kLow for fp16).
 template <bool E4M3>
 __device__ __forceinline__ uint32_t take_part(float& x, float& y) {
   uint32_t d;
   if constexpr (E4M3) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(y), "f"(x));
     const __half2 h = *reinterpret_cast<const __half2*>(&d);
-    x -= __low2float(h);
-    y -= __high2float(h);
+    scale_pair(x, y, kLow);
+    const f2 left = ffma2(f2{__low2float(h), __high2float(h)}, f2{-kLow, -kLow}, f2{x, y});
+    x = left.x, y = left.y;
   } else {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(y), "f"(x));
     x -= __uint_as_float(d << 16);
@@ -532,7 +545,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
       for (int nt = 0; nt < NT; ++nt) {
         float up = 1.0f, down = 1.0f;
         if constexpr (S::E4M3) {
-          // fp16 parts: the head's largest entry is brought to [2^9, 2^10)
+          // fp16 parts: the head's largest entry is brought to [2^14, 2^15) (from 2^-86 on)
           float top = 0.0f;
 #pragma unroll
           for (int ks = 0; ks < S::KS; ++ks) {
@@ -543,7 +556,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
           const int e = (int)(__float_as_uint(top) >> 23) - 127;  // -127: zero or subnormal, 128: inf
           if (e < 128) {
-            const int k = min(100, 9 - e);
+            const int k = min(100, 14 - e);
             up = __uint_as_float((uint32_t)(k + 127) << 23);
             down = __uint_as_float((uint32_t)(127 - k) << 23);
           }
@@ -773,7 +786,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[mt][k] = (acc[mt][nt][1][k] + acc[mt][nt][0][k]) * f1[nt][k & 1];
+            for (int k = 0; k < 4; ++k) s[mt][k] = fmaf(acc[mt][nt][1][k], 1.0f / S::LOW, acc[mt][nt][0][k]) * f1[nt][k & 1];
             if (f2 > 0.0f) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) s[mt][k] = tanh_flat(s[mt][k]) * f2;
@@ -883,7 +896,11 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
             for (int nt = 0; nt < NT; ++nt) {
               float t[4];
 #pragma unroll
-              for (int k = S::PARTS - 1; k >= 0; --k)
+              for (int k = S::PARTS - 1; k >= 0; --k) {
+                if (S::E4M3 && k == 0) {  // the lower parts' sum, back to its size
+                  scale_pair(t[0], t[1], 1.0f / S::LOW);
+                  scale_pair(t[2], t[3], 1.0f / S::LOW);
+                }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                   const uint32_t* a = CAREFUL && k > 0 ? fin[mt] : x[mt];
@@ -892,6 +909,7 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
                   else
                     mma16816<S::E4M3, false>(t, a, pb[mt][nt][k][0], pb[mt][nt][k][1]);
                 }
+              }
 #pragma unroll
               for (int k = 0; k < 4; ++k) o[nt][4 * j + q][k] += t[k];
             }
