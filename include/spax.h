@@ -552,7 +552,8 @@ typedef struct {
  *   d_out[i][h] = sum_j softmax(s)_j v_j (fp32 [n_seq][n_heads][head_dim], fully written),
  *   d_lse[i][h] = ln sum_j exp(s_j) (fp32 [n_seq][n_heads], may be NULL).
  * Queries hold finite entries up to 3.38e38: a head with an infinity or a NaN is NaN where it sees
- * anything (one with a larger finite entry may be), and no other head.
+ * anything (one with a larger finite entry may be), and no other head. Products of a finite query
+ * entry and key entry, and their sums, must not overflow fp32.
  * L = 0 gives out = 0 and lse = -inf, and so does a row whose scores are all -inf. Rows of the
  * cache past L, and outside the window, are not read: what they hold cannot matter.
  * L outside [0, max_pages * page_size] is taken as 0, a page outside [0, n_pages) as not seen, and

@@ -159,13 +159,12 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real, u
                "r"(real ? 16 : 0), "l"(policy));
 }
 
-// Pairs of bf16 elements with an infinity replaced by the largest finite value: what the lower parts
-// of a query or probability multiply in a careful pass. Such a part can be zero or negative, and an
-// infinity times it would turn the product's own infinity into NaN.
+// Pairs of bf16 elements with 0 in place of an infinity: what the lower parts of a query or probability
+// multiply in a careful pass. Such a part can be zero or of the other sign, and an infinity times it
+// would turn the infinity that the first part gives into NaN (so would sums of the largest finite value).
 __device__ __forceinline__ void finite_pairs(const uint32_t (&a)[4], uint32_t (&f)[4]) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(f[k]) : "r"(a[k]), "r"(0x7F7F7F7Fu));
+  for (int k = 0; k < 4; ++k) f[k] = a[k] & ~__vcmpeq2(a[k] & 0x7FFF7FFFu, 0x7F807F80u);
 }
 
 // tanh without branches, within a few ulp: (1 - u) / (1 + u) with u = e^(-2|x|), and below 0.4, where
