@@ -2,6 +2,7 @@
 kernel)."""
 import pytest
 
+from test_layer_host import append, attention, residual
 from tiered_weight_gemv_b200 import spax
 
 SMS = 148
@@ -35,3 +36,10 @@ def test_attention_plans_refuse():
                    dict(max_positions=(1 << 30) + 1), dict(window=-1), dict(sm_count=0)):
         with pytest.raises(spax.SpaxError):
             spax.spax_attention_plan_sms(**{**ok, **change})
+
+
+def test_empty_tensors_have_null_pointers():
+    assert append(n=0, q=None, k=None, v=None, q_out=None, seq=None, pos=None, H=4) == spax.OK
+    assert append(n=0, q=None, k=None, v=None, q_out=None, seq=None, pos=None, table=None, n_seq=0) == spax.OK
+    assert attention(n=0, q=None, out=None, lens=None, table=None) == spax.OK
+    assert residual(n=0, h=None, y=None, r=None, x=None) == spax.OK

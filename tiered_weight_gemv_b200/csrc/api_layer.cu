@@ -67,8 +67,8 @@ spax_status spax_kv_append(const spax_kv_cache* h_cache, const float* q, int64_t
   if (st != SPAX_OK) return st;
   if (n_tok < 0 || n_seq < 0 || n_heads < 0 || n_heads > 65536) return SPAX_ERR_SHAPE;
   if (a.cache.n_kv_heads > 65536) return SPAX_ERR_SHAPE;
+  if (n_tok == 0) return SPAX_OK;  // no pointer counts: those of empty tensors are null
   if ((n_heads == 0) != (q == nullptr)) return SPAX_ERR_ARG;
-  if (n_tok == 0) return SPAX_OK;
   if (!pos || !page_table || n_seq < 1) return SPAX_ERR_ARG;
   if (!seq && n_tok > n_seq) return SPAX_ERR_ARG;
   if (!pages_ok(a.cache, max_pages)) return SPAX_ERR_SHAPE;
