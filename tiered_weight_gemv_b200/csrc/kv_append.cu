@@ -25,6 +25,12 @@ __device__ __forceinline__ float2 turn_of(int pos, double f) {
 
 constexpr int kAppendThreads = 256;
 
+// The turns of a token's pairs, read two at a time in 16 bytes.
+struct alignas(16) Turns {
+  float2 of[128];
+};
+static_assert(alignof(Turns) >= sizeof(float4), "the shared array is placed by its type's alignment");
+
 __device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
   return (uint32_t)to_bf16(x) | ((uint32_t)to_bf16(y) << 16);
 }
@@ -40,7 +46,8 @@ __device__ __forceinline__ uint32_t e4m3_quad(float4 v) {
 // with 2; one token of 96 heads 1.9 us, a chain of three dependent loads.
 template <int N>
 __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const AppendLaunch a) {
-  __shared__ float2 turn[128];
+  __shared__ Turns turns;
+  float2* const turn = turns.of;
   pdl_wait();
   pdl_launch_dependents();
   const int t = blockIdx.x, tid = threadIdx.x;
