@@ -616,7 +616,7 @@ typedef struct {
  * and d_x must differ, and at least one is given. Rows are contiguous. Statistics are in fp32 over
  * values held on the chip, the mean before the deviations (a row's sum of squares must not overflow
  * fp32).
- * Requires 1 <= d <= 32768, 0 <= n_tok <= 2^28 (0: nothing is done), finite scales.
+ * Requires 1 <= d <= 32768, 0 <= n_tok < 2^28 (0: nothing is done), finite scales.
  */
 spax_status spax_residual_norm(const float* d_h, const float* d_y, int n_tok, int d,
                                const spax_norm* h_post, const float* d_gate, int64_t gate_stride,

@@ -43,3 +43,10 @@ def test_empty_tensors_have_null_pointers():
     assert append(n=0, q=None, k=None, v=None, q_out=None, seq=None, pos=None, table=None, n_seq=0) == spax.OK
     assert attention(n=0, q=None, out=None, lens=None, table=None) == spax.OK
     assert residual(n=0, h=None, y=None, r=None, x=None) == spax.OK
+
+
+def test_rows_of_eight_ctas_fit_a_grid():
+    """2^28 rows of a cluster of 8 would be 2^31 CTAs, one more than a grid holds."""
+    assert residual(n=1 << 28, d=32768) == spax.ERR_SHAPE
+    assert residual(n=1 << 28, d=64) == spax.ERR_SHAPE
+    assert 8 * ((1 << 28) - 1) <= 2 ** 31 - 1

@@ -45,6 +45,9 @@ static bool rows_ok(const float* p, int64_t stride, int64_t width, int n) {
   return p && aligned16(p) && (n <= 1 || (stride >= width && stride <= kMaxStride && stride % 4 == 0));
 }
 
+// Rows of a residual norm: 8 CTAs (the most that a row takes) for each stay below 2^31, a grid's limit.
+constexpr int kMaxRows = 1 << 28;
+
 static bool overlap(const float* a, long long na, const float* b, long long nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + 4 * nb && y < x + 4 * na;
@@ -193,7 +196,7 @@ spax_status spax_residual_norm(const float* h, const float* y, int n_tok, int d,
   spax_status st = check_norm(h_post);
   if (st == SPAX_OK) st = check_norm(h_pre);
   if (st != SPAX_OK) return st;
-  if (n_tok < 0 || n_tok > (1 << 28) || d < 1 || d > 32768) return SPAX_ERR_SHAPE;
+  if (n_tok < 0 || n_tok >= kMaxRows || d < 1 || d > 32768) return SPAX_ERR_SHAPE;
   if (!std::isfinite(res_scale) || !std::isfinite(out_scale)) return SPAX_ERR_ARG;
   if (n_tok == 0) return SPAX_OK;
   if (!h || (!r && !x) || (!y && (h_post || gate))) return SPAX_ERR_ARG;
