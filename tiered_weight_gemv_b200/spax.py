@@ -509,13 +509,36 @@ def _row_stride(t: torch.Tensor, n: int, heads: int, d: int, name: str) -> int:
     return row
 
 
-class KvCache:
+class _Described:
+    """What a call's descriptor is formed from. It is formed once, so its attributes are fixed with it; a
+    tensor whose storage is replaced under it (t.data = ..., a module moved or cast) is seen by its
+    address at the next call, and the descriptor is formed again, with its checks."""
+
+    def __init__(self, **given):
+        self.__dict__.update(given)
+        self.__dict__.update(self._form())
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{type(self).__name__}.{name} is fixed; make a new {type(self).__name__}")
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
+
+    def _again(self):
+        self.__dict__.update(self._form())
+
+
+class KvCache(_Described):
     """A paged key-value cache of one layer: keys and values as [n_pages, page_size, n_kv_heads,
     head_dim] tensors of bfloat16 or float8_e4m3fn, views with any order of the outer dimensions
     (both with the same strides). An 8-bit element stands for its value times k_scale / v_scale."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: float = 1.0,
                  v_scale: float = 1.0):
+        super().__init__(k=k, v=v, k_scale=k_scale, v_scale=v_scale)
+
+    def _form(self):
+        k, v = self.k, self.v
         kinds = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3}
         if not k.is_cuda or not v.is_cuda or k.device != v.device:
             raise TypeError("the cache's pools must be CUDA tensors of one device")
@@ -524,14 +547,21 @@ class KvCache:
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
             raise ValueError("the cache's pools must be [n_pages, page_size, n_kv_heads, head_dim] "
                              "with the same strides, the last of them 1")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = k.shape
-        self.dtype, self.device, self._dev = kinds[k.dtype], k.device, k.get_device()
-        self._desc = spax_kv_cache(*k.shape, self.dtype, k_scale, v_scale, 0, *k.stride()[:3],
-                                   k.data_ptr(), v.data_ptr())
-        self._ref = ctypes.byref(self._desc)
+        dtype, at = kinds[k.dtype], (k.data_ptr(), v.data_ptr())
+        desc = spax_kv_cache(*k.shape, dtype, self.k_scale, self.v_scale, 0, *k.stride()[:3], *at)
+        return dict(zip(("n_pages", "page_size", "n_kv_heads", "head_dim"), k.shape), dtype=dtype,
+                    device=k.device, _dev=k.get_device(), _k_at=at[0], _v_at=at[1], _k_now=k.data_ptr,
+                    _v_now=v.data_ptr, _desc=desc, _ref=ctypes.byref(desc))
+
+    def _for(self, dev: int):
+        if self._k_now() != self._k_at or self._v_now() != self._v_at:
+            self._again()
+        if self._dev != dev:
+            raise ValueError(f"the cache is on cuda:{self._dev}, the current device is cuda:{dev}")
+        return self._ref
 
     def desc(self) -> spax_kv_cache:
+        self._for(self._dev)
         return self._desc
 
 
@@ -549,39 +579,55 @@ def alloc_kv_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
     return KvCache(k, v, k_scale, v_scale)
 
 
-class Rope:
+class Rope(_Described):
     """Rotation by position: inv_freq, fp64 [rot_dim / 2] on the device, the radians per position
     of each pair; pairs (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved."""
 
     def __init__(self, inv_freq: torch.Tensor, interleaved: bool = False):
-        dev = inv_freq.get_device()
-        _refuse(torch.float64, dev, inv_freq=inv_freq)
-        self.inv_freq, self.interleaved, self._dev = inv_freq, bool(interleaved), dev
-        self._desc = spax_rope(2 * inv_freq.numel(), int(self.interleaved), inv_freq.data_ptr())
-        self._ref = ctypes.byref(self._desc)
+        super().__init__(inv_freq=inv_freq, interleaved=bool(interleaved))
+
+    def _form(self):
+        f = self.inv_freq
+        dev = f.get_device()
+        _refuse(torch.float64, dev, inv_freq=f)
+        desc = spax_rope(2 * f.numel(), int(self.interleaved), f.data_ptr())
+        return dict(_dev=dev, _at=f.data_ptr(), _now=f.data_ptr, _desc=desc, _ref=ctypes.byref(desc))
+
+    def _for(self, dev: int):
+        if self._now() != self._at:
+            self._again()
+        if self._dev != dev:
+            raise ValueError(f"the rope is on cuda:{self._dev}, the current device is cuda:{dev}")
+        return self._ref
 
 
-class Norm:
+class Norm(_Described):
     """A norm's kind (NORM_RMS or NORM_LAYER), eps, and its weight and bias ([d], both fp32 or both
     bf16; None: none)."""
 
     def __init__(self, weight=None, bias=None, eps: float = 1e-5, kind: int = NORM_RMS):
-        given = [t for t in (weight, bias) if t is not None]
+        super().__init__(weight=weight, bias=bias, eps=eps, kind=kind)
+
+    def _form(self):
+        given = [t for t in (self.weight, self.bias) if t is not None]
         types = {t.dtype for t in given} or {torch.float32}
         if len(types) != 1 or not types <= {torch.float32, torch.bfloat16}:
             raise TypeError("weight and bias must both be float32 or both bfloat16")
         if len({t.numel() for t in given}) > 1:
             raise ValueError("weight and bias must have the same size")
-        self.weight, self.bias, self.eps, self.kind = weight, bias, eps, kind
-        self.d = given[0].numel() if given else None
-        self.device = given[0].get_device() if given else None
+        d = given[0].numel() if given else None
+        device = given[0].get_device() if given else None
         dt = types.pop()
-        _refuse(dt, self.device, weight=weight, bias=bias)
-        ptrs = [None if t is None else t.data_ptr() for t in (weight, bias)]
-        self._desc = spax_norm(kind, int(dt == torch.bfloat16), *ptrs, eps)
-        self._ref = ctypes.byref(self._desc)
+        _refuse(dt, device, weight=self.weight, bias=self.bias)
+        now = [int if t is None else t.data_ptr for t in (self.weight, self.bias)]  # int(): 0, no address
+        at = [f() for f in now]
+        desc = spax_norm(self.kind, int(dt == torch.bfloat16), *at, self.eps)
+        return dict(d=d, device=device, _w_at=at[0], _b_at=at[1], _w_now=now[0], _b_now=now[1], _desc=desc,
+                    _ref=ctypes.byref(desc))
 
     def _for(self, d: int, dev: int):
+        if self._w_now() != self._w_at or self._b_now() != self._b_at:
+            self._again()
         if self.d is not None and (self.d != d or self.device != dev):
             raise ValueError(f"the norm's weight has {self.d} entries on cuda:{self.device}, "
                              f"the rows {d} on cuda:{dev}")
@@ -595,8 +641,9 @@ def spax_kv_append(cache: KvCache, q, k: torch.Tensor, v: torch.Tensor, pos: tor
     [tokens, n_kv_heads, head_dim], fp32, the tokens' strides free (parts of one qkv row); q None:
     keys and values alone. q_out None: q is rotated in place. pos, seq int32 [tokens] (seq None:
     token t is of sequence t), page_table int32 [sequences, pages]; pos < 0 marks padding."""
-    dev, d, heads_kv = _device(), cache.head_dim, cache.n_kv_heads
-    n = pos.numel()
+    dev = _device()
+    ref = cache._for(dev)
+    d, heads_kv, n = cache.head_dim, cache.n_kv_heads, pos.numel()
     ks = _row_stride(k, n, heads_kv, d, "k")
     vs = _row_stride(v, n, heads_kv, d, "v")
     heads = qs = os_ = 0
@@ -631,11 +678,9 @@ def spax_kv_append(cache: KvCache, q, k: torch.Tensor, v: torch.Tensor, pos: tor
             raise ValueError("seq's size does not match pos")
     elif n_seq < n:
         raise ValueError("page_table has fewer rows than there are tokens")
-    if cache._dev != dev or (rope is not None and rope._dev != dev):
-        raise ValueError(f"the cache or rope is not on the current device, cuda:{dev}")
     st = _lib.spax_kv_append(
-        cache._ref, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, n, heads, sq, pos.data_ptr(),
-        page_table.data_ptr(), n_seq, max_pages, None if rope is None else rope._ref, op, os_,
+        ref, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, n, heads, sq, pos.data_ptr(),
+        page_table.data_ptr(), n_seq, max_pages, None if rope is None else rope._for(dev), op, os_,
         status.data_ptr(), _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise SpaxError("spax_kv_append", st)
@@ -671,8 +716,9 @@ def spax_paged_attention(cache: KvCache, q: torch.Tensor, page_table: torch.Tens
     """Attention of one new token of each sequence over the cache: q fp32 [sequences, heads,
     head_dim] (the sequences' stride free), seq_lens int32 [sequences] counting the new token, out
     fp32 as q, contiguous; lse (optional) fp32 [sequences, heads]."""
-    dev, d = _device(), cache.head_dim
-    n = seq_lens.numel()
+    dev = _device()
+    ref = cache._for(dev)
+    d, n = cache.head_dim, seq_lens.numel()
     heads = q.shape[1] if q.dim() == 3 else 0
     qs = _row_stride(q, n, heads, d, "q")
     n_seq, max_pages = page_table.shape
@@ -691,10 +737,8 @@ def spax_paged_attention(cache: KvCache, q: torch.Tensor, page_table: torch.Tens
         _refuse(_i32, dev, page_table=page_table, seq_lens=seq_lens, status=status)
     if ws.dtype is not _u8 or ws.get_device() != dev or not ws.is_contiguous():
         _refuse(_u8, dev, ws=ws)
-    if cache._dev != dev:
-        raise ValueError(f"the cache is not on the current device, cuda:{dev}")
     st = _lib.spax_paged_attention(
-        cache._ref, q.data_ptr(), qs, n, heads, page_table.data_ptr(), max_pages,
+        ref, q.data_ptr(), qs, n, heads, page_table.data_ptr(), max_pages,
         seq_lens.data_ptr(), ctypes.byref(spax_attn_params(scale, softcap, window)),
         out.data_ptr(), None if lse is None else lse.data_ptr(), status.data_ptr(), ws.data_ptr(),
         ws.numel(), _raw_stream(dev) if stream is None else stream.cuda_stream)
