@@ -94,3 +94,12 @@ def test_replaced_storage_is_seen():
     turned = (size + size[..., list(range(32, 64)) + list(range(32))]) * 2.0 ** -21  # as in test_kv_append_gpu
     tol = turned + (abs(want) + turned) * 2.0 ** -8  # and half a step of bf16
     assert (abs(k[at, 15].double().cpu().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("window", [2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 40, -2 ** 31, -2 ** 32 + 1])
+def test_windows_past_32_bits_are_refused(window):
+    """A structure's field keeps the low 32 bits of what it is given."""
+    case = Case([20, 30], 4, 2, 64)
+    with pytest.raises((ValueError, spax.SpaxError)):
+        case.run(window)
+    assert case.status.item() == 0
