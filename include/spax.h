@@ -457,6 +457,8 @@ uint64_t spax_weight_bytes(int d_out, int full_fmt, int64_t n_full, int64_t n_ap
  * the GPU). One layer: norm -> masked GEMV (qkv) -> append -> attention -> masked GEMV (o) -> norm
  * -> masked GEMV (gate/up) -> masked GEMV (down, _swiglu). Activations are fp32 throughout, as the
  * GEMVs take and give them; the calls also take batches and prompts (one row for each token).
+ * Pointers are aligned to their elements where a call asks for no more (else SPAX_ERR_ARG). What a call
+ * reads must not change before it has completed on the GPU (lengths and page tables too).
  * Values are not checked for being finite: a NaN or Inf goes through the formulas (an infinite query
  * entry makes its head NaN).
  */

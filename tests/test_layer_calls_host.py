@@ -1,8 +1,10 @@
 """The decode-layer calls at the edges of what they allow, without a GPU (nothing here launches a
 kernel)."""
+import ctypes
+
 import pytest
 
-from test_layer_host import append, attention, residual
+from test_layer_host import A, append, attention, cache, residual
 from tiered_weight_gemv_b200 import spax
 
 SMS = 148
@@ -50,3 +52,20 @@ def test_rows_of_eight_ctas_fit_a_grid():
     assert residual(n=1 << 28, d=32768) == spax.ERR_SHAPE
     assert residual(n=1 << 28, d=64) == spax.ERR_SHAPE
     assert 8 * ((1 << 28) - 1) <= 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_pointers_off_their_elements_are_refused(off):
+    for name in ("seq", "pos", "table"):
+        assert append(**{name: A + off}) == spax.ERR_ARG
+    for name in ("table", "lens"):
+        assert attention(**{name: A + off}) == spax.ERR_ARG
+    for name, at in (("h", 1), ("y", 2), ("r", 3), ("x", 4), ("gate", 8)):
+        assert residual(**{name: at * A + off}) == spax.ERR_ARG
+    # the calls' outputs that the helpers leave out: lse and the status word
+    c, prm = ctypes.byref(cache()), ctypes.byref(spax.spax_attn_params(0.1, 0.0, 0))
+    for lse, status in ((A + off, None), (None, A + off)):
+        assert spax._lib.spax_paged_attention(c, A, 256, 3, 4, A, 4, A, prm, 4 * A, lse, status, A, 1 << 30,
+                                              None) == spax.ERR_ARG
+    assert spax._lib.spax_kv_append(c, A, 256, A, 128, A, 128, 3, 4, A, A, A, 3, 4, None, A, 256, A + off,
+                                    None) == spax.ERR_ARG

@@ -40,6 +40,12 @@ static bool pages_ok(const spax_kv_cache& c, int max_pages) {
 
 constexpr int64_t kMaxStride = 1ll << 32;  // of rows: the last row's offset fits 64 bits
 
+// Pointers to 4-byte elements (NULL too).
+template <class... T>
+static bool aligned4(const T*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ... | 0) & 3u) == 0;
+}
+
 // Rows of `width` floats: aligned for 16-byte accesses, and apart from one another.
 static bool rows_ok(const float* p, int64_t stride, int64_t width, int n) {
   return p && aligned16(p) && (n <= 1 || (stride >= width && stride <= kMaxStride && stride % 4 == 0));
@@ -74,6 +80,7 @@ spax_status spax_kv_append(const spax_kv_cache* h_cache, const float* q, int64_t
   if ((n_heads == 0) != (q == nullptr)) return SPAX_ERR_ARG;
   if (!pos || !page_table || n_seq < 1) return SPAX_ERR_ARG;
   if (!seq && n_tok > n_seq) return SPAX_ERR_ARG;
+  if (!aligned4(seq, pos, page_table, status)) return SPAX_ERR_ARG;
   if (!pages_ok(a.cache, max_pages)) return SPAX_ERR_SHAPE;
   const int64_t D = a.cache.head_dim, kv = a.cache.n_kv_heads * D;
   if (q && (!rows_ok(q, q_stride, n_heads * D, n_tok) ||
@@ -150,6 +157,7 @@ spax_status spax_paged_attention(const spax_kv_cache* h_cache, const float* q, i
   if (n_heads % a.cache.n_kv_heads != 0) return SPAX_ERR_SHAPE;
   if (n_seq == 0) return SPAX_OK;
   if (!page_table || !seq_lens || !out || !aligned16(out)) return SPAX_ERR_ARG;
+  if (!aligned4(page_table, seq_lens, lse, status)) return SPAX_ERR_ARG;
   if (!pages_ok(a.cache, max_pages)) return SPAX_ERR_SHAPE;
   const int64_t width = (int64_t)n_heads * a.cache.head_dim;
   if (!rows_ok(q, q_stride, width, n_seq)) return SPAX_ERR_ARG;
@@ -199,7 +207,7 @@ spax_status spax_residual_norm(const float* h, const float* y, int n_tok, int d,
   if (n_tok < 0 || n_tok >= kMaxRows || d < 1 || d > 32768) return SPAX_ERR_SHAPE;
   if (!std::isfinite(res_scale) || !std::isfinite(out_scale)) return SPAX_ERR_ARG;
   if (n_tok == 0) return SPAX_OK;
-  if (!h || (!r && !x) || (!y && (h_post || gate))) return SPAX_ERR_ARG;
+  if (!h || (!r && !x) || (!y && (h_post || gate)) || !aligned4(h, y, gate, r, x)) return SPAX_ERR_ARG;
   if (gate && gate_stride != 0 && (gate_stride < d || gate_stride > kMaxStride)) return SPAX_ERR_ARG;
   // outputs may be an input as a whole, and nothing else
   const long long n = (long long)n_tok * d;
