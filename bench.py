@@ -901,10 +901,11 @@ LAYER_CONTEXTS = (512, 4096)
 
 def run_decode_layer(args, dev):
     """The whole decoder layer of the headline's block as a decoder runs it, one token at a time:
-    residual norm, qkv, cache append with rotation, attention over the paged cache, o, residual
-    norm, gate/up, down (fed in its own launch), residual sum. Each token reads its own weight
-    replica and cache, so all of it streams from HBM. Beside it, the four projections alone on the
-    same inputs: the difference is what the steps between them add."""
+    qkv, cache append with rotation, attention over the paged cache, o, residual norm, gate/up, down
+    (fed in its own launch), and the last residual sum with the next layer's first norm, which are one
+    call (so a layer begins with its normed input at hand). Each token reads its own weight replica and
+    cache, so all of it streams from HBM. Beside it, the four projections alone on the same inputs: the
+    difference is what the steps between them add."""
     from tiered_weight_gemv_b200 import spax, synth
 
     n_tok, n_rep = 16, 4
@@ -929,7 +930,8 @@ def run_decode_layer(args, dev):
     rope = spax.Rope(10000.0 ** (-torch.arange(HEAD_DIM // 2, dtype=torch.float64, device=dev)
                                  / (HEAD_DIM // 2)))
     h = synth.laplace((n_tok, 1, HIDDEN), 0, 801, device=dev)
-    x1, r, x2, r2 = (torch.empty_like(h) for _ in range(4))
+    x1, r, x2, r2, x3 = (torch.empty_like(h) for _ in range(5))
+    spax.spax_residual_norm(h, None, None, x1, pre=norm)
     att = torch.empty(n_tok, 1, HEADS, HEAD_DIM, device=dev)
     out = {"tokens": n_tok, "weight_replicas": n_rep, "heads": HEADS, "head_dim": HEAD_DIM,
            "cache": "bf16, pages of %d" % KV_PAGE}
@@ -957,7 +959,7 @@ def run_decode_layer(args, dev):
         table = torch.randperm(pages, device=dev).int().view(1, pages)
         pos = torch.full((1,), ctx - 1, dtype=torch.int32, device=dev)
         lens = torch.full((1,), ctx, dtype=torch.int32, device=dev)
-        torch.cuda.synchronize()  # the caches and the table, before `stream` reads them
+        torch.cuda.synchronize()  # the caches, the table and x1, before `stream` reads them
 
         def between(t):  # qkv's row -> the attention's output
             kv = caches[t % n_cache]
@@ -967,14 +969,13 @@ def run_decode_layer(args, dev):
 
         def layer():
             for t in range(n_tok):
-                spax.spax_residual_norm(h[t], None, None, x1[t], pre=norm)
                 gemv("qkv", t, x1[t].view(-1))
                 between(t)
                 gemv("o", t, att[t].view(-1))
                 spax.spax_residual_norm(h[t], sites["o"]["y"][t].view(1, -1), r[t], x2[t], pre=norm)
                 gemv("gate_up", t, x2[t].view(-1))
                 down(t)
-                spax.spax_residual_norm(r[t], sites["down"]["y"][t].view(1, -1), r2[t], None)
+                spax.spax_residual_norm(r[t], sites["down"]["y"][t].view(1, -1), r2[t], x3[t], pre=norm)
 
         def projections():
             for t in range(n_tok):

@@ -103,3 +103,16 @@ def test_windows_past_32_bits_are_refused(window):
     with pytest.raises((ValueError, spax.SpaxError)):
         case.run(window)
     assert case.status.item() == 0
+
+
+@pytest.mark.parametrize("n,d", [(1, 4096), (3, 515), (200, 1028), (2, 16384)])
+def test_a_residual_sum_with_the_next_norm_is_the_two_calls(n, d):
+    """A layer's last sum and the next layer's first norm in one call give the bits of two."""
+    h, y = (torch.randn(n, d, device="cuda") for _ in range(2))
+    for kind in (spax.NORM_RMS, spax.NORM_LAYER):
+        norm = spax.Norm(torch.rand(d, device="cuda"), kind=kind)
+        r, x, r2, x2 = (torch.empty_like(h) for _ in range(4))
+        spax.spax_residual_norm(h, y, r, x, pre=norm)
+        spax.spax_residual_norm(h, y, r2, None)
+        spax.spax_residual_norm(r2, None, None, x2, pre=norm)
+        assert torch.equal(r, r2) and torch.equal(x, x2)
