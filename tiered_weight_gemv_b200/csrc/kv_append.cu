@@ -34,6 +34,7 @@ static_assert(alignof(Turns) >= sizeof(float4), "the shared array is placed by i
 __device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
   return (uint32_t)to_bf16(x) | ((uint32_t)to_bf16(y) << 16);
 }
+// Saturates: past 448 (infinities too) it is 448.
 __device__ __forceinline__ uint32_t e4m3_quad(float4 v) {
   const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(v.x, v.y), __NV_SATFINITE, __NV_E4M3);
   const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(v.z, v.w), __NV_SATFINITE, __NV_E4M3);

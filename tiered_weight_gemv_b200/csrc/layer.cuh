@@ -20,12 +20,9 @@ __device__ __forceinline__ long long cache_row(const spax_kv_cache& c, const int
   return page * c.page_stride + (long long)(pos - at * c.page_size) * c.token_stride;
 }
 
-// One value in the cache's type. E4M3 saturates: past 448 (infinities too) it is 448.
+// One value in the bf16 cache's type.
 __device__ __forceinline__ uint16_t to_bf16(float v) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
-  return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
 }
 
 }  // namespace spax
