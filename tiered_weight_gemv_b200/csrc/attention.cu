@@ -1,9 +1,10 @@
 // attention.cu — attention of one new token of each sequence over the paged key-value cache.
 //
 // For query head h over the positions j that it sees: s_j = scale (q . k_j) (capped when asked),
-// out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m). The cache is read once, 4 G flops for each of its
-// elements (G query heads to a key head), so the bound is HBM; everything else is arranged to keep
-// enough bytes in flight.
+// out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m). The formula takes 2 G flops
+// for each element of the cache (G query heads to a key head), so while the cache is read once the bound
+// is HBM, and everything is arranged to keep enough bytes in flight. It is read once for each block of 8
+// query heads to a key head (16 where G > 8 and heads are up to 128 wide), so again for the next block.
 //
 // Work: a row is one (sequence, key head, block of up to 8 NT query heads). Its positions are cut
 // into units of 64, and the units of all rows are dealt to the CTAs of one wave in nearly equal runs,
@@ -18,8 +19,9 @@
 //
 // Products run on the m16n8k16 matrix instructions, transposed: S^T = K Q^T and O^T = V^T P^T, so
 // that the 16-row side is always positions or entries of the cache and the 8-column side the query
-// heads (a decode step has 1 to 16 heads to a key head; the 128-row tiles of tcgen05 would be idle
-// for the most part, and at 16 flops a byte the smaller instructions are nowhere near their rate).
+// heads. The 128 rows of tcgen05 would be full that way as well; up to 8 heads to a key head, where HBM
+// is the bound, its rate would gain nothing. With more heads, and with 256-wide ones, the outputs'
+// registers leave 8 to 12 warps on an SM, which tensor memory would free: not built.
 // The order of a head's entries along the contraction is free, so a lane takes the 16 bytes that
 // lie together in the cache as the fragment's entries and the query is laid out to match; for V the
 // pairs of positions that a fragment wants are woven from two rows by byte permutes.
@@ -36,11 +38,12 @@
 // kept outside of them. Against 64 bits the outputs are 2e-7 to 7e-7 off (2-norm), less than elementary
 // fp32 operations.
 //
-// Measured on B200 (6.55 TB/s is a copy's rate): 131071 positions of 8 key heads 87 to 90 us, 6.0 to 6.2 TB/s; a
-// ragged batch of 64 up to 8192 113 to 116 us, 6.2 to 6.4 TB/s; 33 x 4099 positions of an 8-bit cache 52 us, 5.4
-// TB/s: there its products and their latency bound it, and the start and end of a CTA, about 3 and
-// 1 us. One token of 32 heads over 517 positions 8.2 us: launch 2,
-// start-up 2 (lengths, dealing, page table), copies and tiles 2, the join of nine parts 1.
+// Measured on B200 (6.55 TB/s is a copy's rate): 131071 positions of 8 key heads 87 to 90 us, 6.0 to 6.2
+// TB/s; a ragged batch of 64 up to 8192 113 to 116 us, 6.2 to 6.4 TB/s; 33 x 4099 positions of an 8-bit
+// cache 52 to 53 us, 5.3 TB/s: there its products and their latency bound it, and the start and end of a
+// CTA, about 3 and 1 us. One token of 32 heads over 517 positions 8.2 us: launch 2, start-up 2 (lengths, dealing, page
+// table), copies and tiles 2, the join of nine parts 1. The ragged batch with 16 heads to a key head 156
+// us (8-bit 114); with 71 heads on one key head, 64-wide, 56 us, eight times what one read would take.
 #include <type_traits>
 
 #include "layer.cuh"
@@ -145,10 +148,11 @@ __device__ __forceinline__ uint32_t take_part(float& x, float& y) {
   return d;
 }
 
-// The cache is read once a token and is the first to leave L2 again. Else 67 MB of it push out what the
+// A token's reads of the cache are the first to leave L2 again. Else 67 MB of it push out what the
 // projections around the call keep there (their code, the activations, their workspaces): a
 // Llama-2-7B layer at a context of 4096 takes 109 us a token then and 96 so, the attention alone
-// 116 and 113 (ragged batch of 64 up to 8192).
+// 116 and 113 (ragged batch of 64 up to 8192). Where blocks of heads read it again the mark costs
+// nothing on the whole (-4 to +5% without it over nine batches of 2 to 8 blocks).
 __device__ __forceinline__ uint64_t evict_first() {
   uint64_t policy;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
@@ -785,7 +789,8 @@ __global__ void __launch_bounds__(S::THREADS, S::CTAS) attention_kernel(const At
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[mt][k] = fmaf(acc[mt][nt][1][k], 1.0f / S::LOW, acc[mt][nt][0][k]) * f1[nt][k & 1];
+            for (int k = 0; k < 4; ++k)
+              s[mt][k] = fmaf(acc[mt][nt][1][k], 1.0f / S::LOW, acc[mt][nt][0][k]) * f1[nt][k & 1];
             if (f2 > 0.0f) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) s[mt][k] = tanh_flat(s[mt][k]) * f2;
