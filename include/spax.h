@@ -589,7 +589,8 @@ size_t spax_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim)
 /*
  * Host-only, no CUDA call: the CTAs that spax_paged_attention launches on a GPU with sm_count SMs for
  * tables of max_positions (max_pages * page_size) positions a sequence, by the rule that the call uses,
- * and the workspace bytes there. Requires what the call requires of these arguments, n_seq >= 1.
+ * and the workspace bytes there. Requires what the call requires of these arguments, n_seq >= 1 and
+ * sm_count from 1 to 65536.
  */
 spax_status spax_attention_plan_sms(int n_seq, int n_heads, int n_kv_heads, int head_dim, int kv_dtype,
                                     int64_t max_positions, int window, int sm_count, int32_t* ctas,

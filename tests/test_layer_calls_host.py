@@ -35,7 +35,8 @@ def test_attention_plans_refuse():
     assert spax.spax_attention_plan_sms(**ok)[0] == 6  # a row of one unit each
     for change in (dict(n_seq=0), dict(n_seq=65536), dict(n_heads=0), dict(n_heads=7), dict(n_kv_heads=0),
                    dict(head_dim=72), dict(head_dim=512), dict(kv_dtype=2), dict(max_positions=0),
-                   dict(max_positions=(1 << 30) + 1), dict(window=-1), dict(sm_count=0)):
+                   dict(max_positions=(1 << 30) + 1), dict(window=-1), dict(sm_count=0),
+                   dict(sm_count=65537), dict(sm_count=2 ** 31 - 1, max_positions=1 << 30, n_seq=65535)):
         with pytest.raises(spax.SpaxError):
             spax.spax_attention_plan_sms(**{**ok, **change})
 

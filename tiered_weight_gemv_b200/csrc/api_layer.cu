@@ -127,7 +127,7 @@ spax_status spax_attention_plan_sms(int n_seq, int n_heads, int n_kv_heads, int 
                                     int64_t max_positions, int window, int sm_count, int32_t* ctas,
                                     size_t* ws_bytes) {
   if (kv_dtype != SPAX_KV_BF16 && kv_dtype != SPAX_KV_E4M3) return SPAX_ERR_ARG;
-  if (window < 0 || sm_count < 1) return SPAX_ERR_ARG;
+  if (window < 0 || sm_count < 1 || sm_count > 65536) return SPAX_ERR_ARG;  // 4 sm_count CTAs fit an int
   if (n_seq < 1 || n_seq > 65535 || n_heads < 1 || n_heads > 65535) return SPAX_ERR_SHAPE;
   if (n_kv_heads < 1 || n_heads % n_kv_heads != 0) return SPAX_ERR_SHAPE;
   if (head_dim < 16 || head_dim > 256 || head_dim % 16 != 0) return SPAX_ERR_SHAPE;
