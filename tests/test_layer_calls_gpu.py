@@ -54,6 +54,10 @@ def test_what_a_descriptor_is_formed_from_is_fixed():
             with pytest.raises(AttributeError):
                 delattr(obj, name)
             assert getattr(obj, name) is before
+        obj.layer = 7  # a caller's own
+        assert obj.layer == 7
+        del obj.layer
+        assert not hasattr(obj, "layer")
 
 
 def test_replaced_storage_is_seen():

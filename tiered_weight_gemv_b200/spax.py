@@ -517,12 +517,17 @@ class _Described:
     def __init__(self, **given):
         self.__dict__.update(given)
         self.__dict__.update(self._form())
+        self.__dict__["_fixed"] = frozenset(self.__dict__)  # a caller's own attributes are free
 
     def __setattr__(self, name, value):
-        raise AttributeError(f"{type(self).__name__}.{name} is fixed; make a new {type(self).__name__}")
+        if name in self._fixed:
+            raise AttributeError(f"{type(self).__name__}.{name} is fixed; make a new {type(self).__name__}")
+        super().__setattr__(name, value)
 
     def __delattr__(self, name):
-        self.__setattr__(name, None)
+        if name in self._fixed:
+            self.__setattr__(name, None)
+        super().__delattr__(name)
 
     def _again(self):
         self.__dict__.update(self._form())
