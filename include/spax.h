@@ -618,7 +618,7 @@ typedef struct {
  * d_x (NULL: not written, h_pre not used) may be d_y or d_h; h_pre NULL with d_x set: x = r. d_r
  * and d_x must differ, and at least one is given. Rows are contiguous. Statistics are in fp32 over
  * values held on the chip, the mean before the deviations (a row's sum of squares must not overflow
- * fp32).
+ * fp32, nor underflow where eps is 0).
  * Requires 1 <= d <= 32768, 0 <= n_tok < 2^28 (0: nothing is done), finite scales.
  */
 spax_status spax_residual_norm(const float* d_h, const float* d_y, int n_tok, int d,

@@ -740,7 +740,7 @@ def spax_paged_attention(cache: KvCache, q: torch.Tensor, page_table: torch.Tens
             or status.get_device() != dev or not page_table.is_contiguous()
             or not seq_lens.is_contiguous()):
         _refuse(_i32, dev, page_table=page_table, seq_lens=seq_lens, status=status)
-    if not -1 <= window < 1 << 31:  # the structure's field would keep its low 32 bits
+    if not -1 << 31 <= window < 1 << 31:  # the structure's field would keep its low 32 bits
         raise ValueError(f"window must be at least 0 and below 2^31, got {window}")
     if ws.dtype is not _u8 or ws.get_device() != dev or not ws.is_contiguous():
         _refuse(_u8, dev, ws=ws)
