@@ -514,10 +514,17 @@ class _Described:
     tensor whose storage is replaced under it (t.data = ..., a module moved or cast) is seen by its
     address at the next call, and the descriptor is formed again, with its checks."""
 
+    _fixed = frozenset()  # the attributes of a formed object; a caller's own are free
+
     def __init__(self, **given):
-        self.__dict__.update(given)
-        self.__dict__.update(self._form())
-        self.__dict__["_fixed"] = frozenset(self.__dict__)  # a caller's own attributes are free
+        self._put(given)
+        formed = self._form()
+        self._put(formed)
+        self._put({"_fixed": frozenset((*given, *formed, "_fixed"))})
+
+    def _put(self, values):
+        for name, value in values.items():  # not through __dict__, whose use slows later reads
+            object.__setattr__(self, name, value)
 
     def __setattr__(self, name, value):
         if name in self._fixed:
@@ -530,7 +537,7 @@ class _Described:
         super().__delattr__(name)
 
     def _again(self):
-        self.__dict__.update(self._form())
+        self._put(self._form())
 
 
 class KvCache(_Described):
